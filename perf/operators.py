@@ -8,7 +8,7 @@ points.  A cache page holds `page` tokens of every KV head; `table[b, i]` is the
 tokens i * page .. of sequence b.
 
 Quantisation (Q4_0): of 32 consecutive channels of one token and head, m is the first value
-of the largest magnitude, d = -m / 8 limited to the fp16 range, q = floor(x / d + 8.5)
+of the largest magnitude, d = -m / 8 limited to +-8188 (so that 8 |d| stays in the fp16 range), q = floor(x / d + 8.5)
 limited to 0..15, and the cache holds q and fp16(d); it stands for (q - 8) * fp16(d).
 """
 import math
@@ -117,7 +117,7 @@ def _quantise(x):
     """(q, d) of x [..., dim] in blocks of 32 channels: q [..., dim / 32, 32] float, d [..., dim / 32, 1] rounded to fp16."""
     x = x.float().unflatten(-1, (-1, 32))
     m = x.gather(-1, x.abs().argmax(-1, keepdim=True))
-    d = (m / -8).clamp(-65504.0, 65504.0)
+    d = (m / -8).clamp(-8188.0, 8188.0)
     q = torch.floor(x / torch.where(d == 0, torch.ones_like(d), d) + 8.5).clamp(0, 15)
     return q, d.half().float()
 
@@ -329,7 +329,7 @@ def _exact_rows(x):
     x = x.double().reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     big = x.abs().max(-1, keepdim=True)[0]
     first = torch.argmax((x.abs() == big).to(torch.int8), -1, keepdim=True)
-    d = (-torch.gather(x, -1, first) / 8).clamp(-65504, 65504)
+    d = (-torch.gather(x, -1, first) / 8).clamp(-8188, 8188)
     q = torch.where(d == 0, torch.full_like(x, 8.0), torch.floor(x / d + 8.5)).clamp(0, 15)
     return ((q - 8) * d.to(torch.float16).double()).flatten(-2)
 
