@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import atexit
 import ctypes
+import functools
 import os
 import re
 import weakref
@@ -30,6 +31,8 @@ MOE_ERR_DEVICE = -7
 MOE_PIN_HIT, MOE_RING_HIT, MOE_MISS = 0, 1, 2
 MOE_PLACE_CALIBRATED, MOE_PLACE_UNIFORM = 0, 1
 MOE_MISS_COPY_ENGINE, MOE_MISS_SM_PULL = 0, 1
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_DEVERR_PAGE = 7
 
 
 class MoEError(RuntimeError):
@@ -58,6 +61,25 @@ class NoAllocWeights(ctypes.Structure):
     _fields_ = [("experts_dev", ctypes.c_void_p), ("shared_dev", ctypes.c_void_p),
                 ("router_dev", ctypes.c_void_p), ("bias_dev", ctypes.c_void_p),
                 ("gain_dev", ctypes.c_void_p)]
+
+
+class KvPool(ctypes.Structure):
+    _fields_ = [("pool_dev", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("device", ctypes.c_int32),
+                ("error_dev", ctypes.c_void_p)]
+
+
+class KvTable(ctypes.Structure):
+    _fields_ = [("table_dev", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data_dev", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KvScore(ctypes.Structure):
+    _fields_ = [("data_dev", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class Event(ctypes.Structure):
@@ -109,6 +131,18 @@ _SIGS = {
     "moe_debug_drop_signals": (ctypes.c_int, [_P, ctypes.c_int32]),
     "moe_decode_step_noalloc": (ctypes.c_int, [ctypes.POINTER(Config), ctypes.POINTER(NoAllocWeights),
                                                 _P, _P, _P]),
+    "moe_kv_store": (ctypes.c_int, [ctypes.POINTER(KvPool), ctypes.POINTER(KvTable), _P, _P, ctypes.POINTER(Rows),
+                                    ctypes.POINTER(Rows), ctypes.c_int32, ctypes.c_int32, _P]),
+    "moe_kv_load": (ctypes.c_int, [ctypes.POINTER(KvPool), ctypes.POINTER(KvTable), _P, _P, ctypes.POINTER(Rows),
+                                   ctypes.POINTER(Rows), ctypes.c_int32, ctypes.c_int32, _P]),
+    "moe_kv_attend": (ctypes.c_int, [ctypes.POINTER(KvPool), ctypes.POINTER(KvTable), _P, ctypes.c_int32,
+                                     ctypes.POINTER(Rows), ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                     ctypes.POINTER(Rows), ctypes.POINTER(KvScore), _P, ctypes.c_size_t, _P]),
+    "moe_kv_attend_workspace": (ctypes.c_int, [ctypes.POINTER(KvPool), ctypes.POINTER(KvTable), ctypes.c_int32,
+                                               ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_kv_evict": (ctypes.c_int, [ctypes.POINTER(KvPool), ctypes.POINTER(KvTable), _P, ctypes.c_int32,
+                                    ctypes.POINTER(KvScore), ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(KvTable),
+                                    _P, _P, _P, _P]),
     "moe_destroy": (None, [_P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -375,3 +409,191 @@ class ExpertCacheMoE:
     def set_trace(self, h_trace=None, w_trace=None):
         moe_set_trace(self.ctx, None if h_trace is None else h_trace.data_ptr(),
                       None if w_trace is None else w_trace.data_ptr())
+
+
+# ------------------------------------------------------------------ attention operators
+
+_DTYPES = {"torch.bfloat16": MOE_BF16, "torch.float16": MOE_F16, "torch.float32": MOE_F32}
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise MoEError(MOE_ERR_INVALID, what)
+
+
+def _dtype(t, what: str) -> int:
+    d = _DTYPES.get(str(t))
+    _need(d is not None, f"{what}: dtype {t}")
+    return d
+
+
+def _ints(t, dim: int, dev, what: str) -> int:
+    import torch
+    _need(t.dtype == torch.int32 and t.dim() == dim and t.device == dev and (t.shape[-1] <= 1 or t.stride(-1) == 1),
+          f"{what} must be an int32 tensor of {dim} dimension(s) on {dev}, its last one contiguous")
+    return t.data_ptr()
+
+
+def _kv_pool(pool, error, what: str):
+    import torch
+    _need(pool.dtype == torch.uint8 and pool.dim() == 4 and pool.is_cuda and pool.is_contiguous(),
+          f"{what}: pool must be a contiguous uint8 CUDA tensor [pages, KV heads, page tokens / 16, 18 * head dim]")
+    pages, heads, tiles, size = pool.shape
+    _need(size % 18 == 0, f"{what}: pool tiles must have 18 * head dim bytes")
+    err = None if error is None else _ints(error, 1, pool.device, f"{what}: error")
+    return KvPool(pool.data_ptr(), pages, heads, size // 18, tiles * 16, pool.device.index, err)
+
+
+def _kv_table(table, dev, what: str):
+    p = _ints(table, 2, dev, f"{what}: table")
+    return KvTable(p, table.shape[0], table.shape[1], table.stride(0) if table.shape[0] > 1 else table.shape[1])
+
+
+def _rows(t, n, heads, dim, dtype, dev, what: str):
+    _need(tuple(t.shape) == (n, heads, dim) and t.dtype == dtype and t.device == dev and t.stride(2) == 1,
+          f"{what} must be a {dtype} tensor {[n, heads, dim]} on {dev}, its last dimension contiguous")
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _kv_score(score, n, heads, most, dev, what: str):
+    import torch
+    _need(score.dtype == torch.float32 and score.dim() == 3 and tuple(score.shape[:2]) == (n, heads)
+          and score.shape[2] >= most and score.device == dev and (score.shape[2] <= 1 or score.stride(2) == 1),
+          f"{what}: score must be a float32 tensor [{n}, {heads}, >= {most}] on {dev}, its last dimension contiguous")
+    return KvScore(score.data_ptr(), score.stride(0), score.stride(1))
+
+
+def _on(stream, dev):
+    """The stream to launch on and, for buffers allocated here, the context that ties them to it."""
+    import contextlib
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream, contextlib.nullcontext()
+    _need(stream.device == dev, f"the stream is on {stream.device}, the tensors are on {dev}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def kv_pool(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device=0):
+    """A zeroed 4-bit key/value cache: uint8 [n_pages, n_kv_heads, page_tokens / 16, 18 * head_dim]
+    (page_tokens a multiple of 16, head_dim 64 or 128; layout in include/moe_cache.h)."""
+    import torch
+    _need(page_tokens > 0 and page_tokens % 16 == 0, f"kv_pool: page_tokens {page_tokens} is not a multiple of 16")
+    _need(head_dim in (64, 128), f"kv_pool: head_dim {head_dim} is neither 64 nor 128")
+    return torch.zeros((n_pages, n_kv_heads, page_tokens // 16, 18 * head_dim), dtype=torch.uint8,
+                       device=torch.device("cuda", device) if isinstance(device, int) else device)
+
+
+def _kv_rows_call(name, pool, k, v, table, cu, start, n, stream_ptr, error):
+    dev = pool.device
+    c = _kv_pool(pool, error, name)
+    t = _kv_table(table, dev, name)
+    cu_p = _ints(cu, 1, dev, f"{name}: cu")
+    _need(cu.shape[0] == t.n_seqs + 1, f"{name}: cu must have {t.n_seqs + 1} entries")
+    start_p = None
+    if start is not None:
+        start_p = _ints(start, 1, dev, f"{name}: start")
+        _need(start.shape[0] == t.n_seqs, f"{name}: start must have {t.n_seqs} entries")
+    rk = _rows(k, n, c.n_kv_heads, c.head_dim, k.dtype, dev, f"{name}: k")
+    rv = _rows(v, n, c.n_kv_heads, c.head_dim, k.dtype, dev, f"{name}: v")
+    if n:
+        _check(getattr(lib(), "moe_" + name)(c, t, cu_p, start_p, rk, rv, n, _dtype(k.dtype, name), stream_ptr), "moe_" + name)
+
+
+def kv_store(pool, k, v, table, cu, start=None, error=None, stream=None) -> None:
+    """Quantise rows k, v [tokens, KV heads, head dim] (bf16, fp16 or fp32) into the cache:
+    rows cu[b] .. cu[b + 1] - 1 go to positions start[b] .. (0 .. without start) of sequence
+    b, whose pages are table[b].  Rows outside cu[0] .. cu[-1] are padding.  error: int32
+    [1], receives MOE_DEVERR_PAGE when a row has no place in the cache (that row is skipped)."""
+    s, _ = _on(stream, pool.device)
+    _kv_rows_call("kv_store", pool, k, v, table, cu, start, k.shape[0], s, error)
+
+
+def kv_load(pool, table, cu, start, n_tokens: int, dtype, out=None, error=None, stream=None):
+    """Read cached rows back as the values they stand for, addressed as in kv_store.  Returns
+    (k, v) [n_tokens, KV heads, head dim]; out: that pair of tensors to write to.  Padding
+    rows are left as they were (unspecified in tensors made here)."""
+    import torch
+    s, ctx = _on(stream, pool.device)
+    if out is None:
+        shape = (n_tokens, pool.shape[1], pool.shape[3] // 18)
+        with ctx:
+            out = torch.empty(shape, dtype=dtype, device=pool.device), torch.empty(shape, dtype=dtype, device=pool.device)
+    _need(out[0].dtype == dtype, f"kv_load: out must be {dtype}")
+    _kv_rows_call("kv_load", pool, out[0], out[1], table, cu, start, n_tokens, s, error)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _attend_workspace(heads, dim, page, device, n_seqs, width, n_q_heads, max_len, scored) -> int:
+    n = ctypes.c_size_t(0)
+    # sizes alone: the addresses only have to be non-null and aligned
+    _check(lib().moe_kv_attend_workspace(KvPool(256, 1, heads, dim, page, device, None), KvTable(256, n_seqs, width, width),
+                                         n_q_heads, max_len, scored, n), "moe_kv_attend_workspace")
+    return n.value
+
+
+def kv_attend(pool, q, table, lens, max_len=None, scale=None, score=None, out=None, workspace=None, error=None,
+              stream=None):
+    """Attention of one token per sequence, q [sequences, query heads, head dim] (bf16 or
+    fp16), over the first lens[b] cached positions of each.  max_len: an upper bound of lens
+    known here (default: all that table holds); scale: default head_dim ** -0.5.  score:
+    float32 [sequences, KV heads, >= max_len], to which every position's weight, summed
+    over the query heads of its KV head, is added.  workspace: uint8 tensor of at least
+    kv_attend_workspace(...) bytes for callers that keep their own; made here otherwise.
+    Returns out (q's shape and type); a sequence of length 0 gives zeros, one whose length
+    or pages lie outside the cache NaN (and error, int32 [1], MOE_DEVERR_PAGE)."""
+    import torch
+    dev = pool.device
+    c = _kv_pool(pool, error, "kv_attend")
+    t = _kv_table(table, dev, "kv_attend")
+    lens_p = _ints(lens, 1, dev, "kv_attend: lens")
+    _need(lens.shape[0] == t.n_seqs and q.dim() == 3, f"kv_attend: lens must have {t.n_seqs} entries, q three dimensions")
+    n, heads, dim = t.n_seqs, q.shape[1], c.head_dim
+    most = t.width * c.page_tokens if max_len is None else int(max_len)
+    rq = _rows(q, n, heads, dim, q.dtype, dev, "kv_attend: q")
+    sc = None if score is None else _kv_score(score, n, c.n_kv_heads, most, dev, "kv_attend")
+    s, ctx = _on(stream, dev)
+    need = _attend_workspace(c.n_kv_heads, dim, c.page_tokens, c.device, n, t.width, heads, most, int(score is not None))
+    with ctx:
+        if out is None:
+            out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace.device == dev and workspace.is_contiguous(), f"kv_attend: workspace must be contiguous on {dev}")
+    ro = _rows(out, n, heads, dim, q.dtype, dev, "kv_attend: out")
+    if n:
+        _check(lib().moe_kv_attend(c, t, lens_p, most, rq, heads, _dtype(q.dtype, "kv_attend"),
+                                   dim ** -0.5 if scale is None else scale, ro, sc, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), s), "moe_kv_attend")
+    return out
+
+
+def kv_attend_workspace(pool, table, n_q_heads: int, max_len: int, scored: bool = False) -> int:
+    """Bytes of workspace that kv_attend needs for these sizes."""
+    return _attend_workspace(pool.shape[1], pool.shape[3] // 18, pool.shape[2] * 16, pool.device.index, table.shape[0],
+                             table.shape[1], n_q_heads, max_len, int(scored))
+
+
+def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out_table, error=None, stream=None):
+    """Cut every sequence and KV head down to `keep` positions: the last `recent` and, of the
+    others, those of the largest score (ties: the lower position).  The kept rows are
+    copied in order to the pages of out_table (pages that table does not name).  Returns
+    (lengths int32 [sequences], former positions int32 [sequences, KV heads, keep], scores
+    float32 of the same shape); behind a sequence's end positions are -1, scores 0."""
+    import torch
+    dev = pool.device
+    c = _kv_pool(pool, error, "kv_evict")
+    t, o = _kv_table(table, dev, "kv_evict"), _kv_table(out_table, dev, "kv_evict: out_table")
+    lens_p = _ints(lens, 1, dev, "kv_evict: lens")
+    _need(lens.shape[0] == t.n_seqs, f"kv_evict: lens must have {t.n_seqs} entries")
+    sc = _kv_score(score, t.n_seqs, c.n_kv_heads, max_len, dev, "kv_evict")
+    _need(keep >= 1, f"kv_evict: keep {keep}")
+    s, ctx = _on(stream, dev)
+    with ctx:
+        out_lens = torch.empty(t.n_seqs, dtype=torch.int32, device=dev)
+        kept = torch.empty((t.n_seqs, c.n_kv_heads, keep), dtype=torch.int32, device=dev)
+        out_score = torch.empty((t.n_seqs, c.n_kv_heads, keep), dtype=torch.float32, device=dev)
+    if t.n_seqs:
+        _check(lib().moe_kv_evict(c, t, lens_p, max_len, sc, keep, recent, o, out_lens.data_ptr(), kept.data_ptr(),
+                                  out_score.data_ptr(), s), "moe_kv_evict")
+    return out_lens, kept, out_score

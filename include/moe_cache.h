@@ -135,6 +135,13 @@ typedef struct {
 #define MOE_DEVERR_SLOT 5    /* an expert had no slot (cold with an empty ring) */
 #define MOE_DEVERR_RANGE 6   /* a unit's share of a layer output was not finite or |v| >= 2^26 */
 
+#define MOE_DEVERR_PAGE 7  /* a page number, position or length outside the cache that was described */
+
+/* Element types of the attention operators' rows. */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_F32 2 /* moe_kv_store and moe_kv_load only */
+
 /* Miss-path variants for moe_set_miss_path. */
 #define MOE_MISS_COPY_ENGINE 0 /* host proxy thread + cudaMemcpyAsync on a side stream (default) */
 #define MOE_MISS_SM_PULL 1     /* the kernel's CTAs read the expert from mapped pinned host memory */
@@ -344,6 +351,116 @@ typedef struct {
  * writes NaN to every element of y_dev, since this entry point has no moe_sync. */
 MOE_API int moe_decode_step_noalloc(const moe_config *cfg, const moe_noalloc_weights *w,
                                     const float *x_dev, float *y_dev, void *stream);
+
+/* ---------------------------------------------------------------- attention operators
+ *
+ * The other half of a layer: attention over keys and values that are cached in 4 bits (the
+ * Baidu MoE page's "KV cache" use of Q4_0, quantisation section), bounded like the expert
+ * cache by what has been used most, and the causal attention of whole prompts that fills
+ * it.  These calls take no context: every buffer is the caller's, nothing is allocated and
+ * no call waits for the device, so each can be captured into a graph.  Tensors live on
+ * the device named in the descriptor (or argument), which need not be the current one; work is
+ * enqueued on stream, a stream of that device.  Calls on one host thread or several, on
+ * one stream or several, do not disturb one another as long as the caller orders those
+ * that share buffers (a workspace among them).
+ *
+ * Positions, lengths and page numbers live on the device, where the host cannot check
+ * them: the kernels do.  A row whose page number, position or length lies outside the
+ * described cache is neither read nor written there; error_dev (when not NULL) receives
+ * MOE_DEVERR_PAGE if it was 0, and the call's results for that row (moe_kv_load) or that
+ * sequence (moe_kv_attend) are NaN. */
+
+/* A cache pool: n_pages pages of page_tokens tokens (a multiple of 16) of every KV head,
+ * head_dim 64 or 128, pool_dev 16-byte aligned:
+ *   [n_pages][n_kv_heads][page_tokens / 16] tiles of 18 * head_dim bytes.
+ * A tile holds 16 tokens of one head.  With NB = head_dim / 32 Q4_0 blocks a token and the
+ * canonical 16 nibble bytes of a block numbered 0..15 (byte j: channel j in the low half,
+ * channel j + 16 in the high one):
+ *   [16 tokens][4 words t][NB][key bytes 4t..4t+3]
+ *   [8 token pairs][8 words g][NB][2 tokens][value bytes 2g, 2g+1]
+ *   [16 tokens][NB] fp16 key scales, [8 token pairs][NB][2 tokens] fp16 value scales.
+ * Quantisation, per token, head and 32 channels: m = the first value of the largest
+ * magnitude, d = -m / 8 limited to [-8188, 8188], q = floor(x / d + 8.5) limited to 0..15
+ * (8 when d = 0); the cache holds q and fp16(d) and stands for (q - 8) * fp16(d).  A NaN
+ * makes its whole block NaN. */
+typedef struct {
+  uint8_t *pool_dev;
+  int32_t n_pages, n_kv_heads, head_dim, page_tokens;
+  int32_t device;
+  int32_t *error_dev; /* device word, caller-owned, or NULL */
+} moe_kv_pool;
+
+/* Page table: page table_dev[b * row_stride + i] holds positions i * page_tokens .. of
+ * sequence b; width entries a sequence are valid to read.  At most 8192 sequences. */
+typedef struct {
+  const int32_t *table_dev;
+  int32_t n_seqs, width;
+  int64_t row_stride;
+} moe_kv_table;
+
+/* Rows [tokens][heads][head_dim], the last dimension contiguous, strides in elements. */
+typedef struct {
+  void *data_dev;
+  int64_t token_stride, head_stride;
+} moe_rows;
+
+/* Accumulated attention weights [n_seqs][n_kv_heads][max_len] fp32, the last contiguous. */
+typedef struct {
+  float *data_dev;
+  int64_t seq_stride, head_stride;
+} moe_kv_score;
+
+/* Quantise rows into the cache.  The n_tokens rows of k and v are those of all sequences
+ * in a row: rows cu_dev[b] .. cu_dev[b + 1] - 1 (cu_dev: n_seqs + 1 int32, ascending) go to
+ * positions start_dev[b] .. of sequence b (start_dev: n_seqs int32, NULL = all 0).  Rows
+ * below cu_dev[0] and from cu_dev[n_seqs] on are padding and not read.  Only the bytes of
+ * the rows' own positions change.  Two sequences of one call whose tables name the same
+ * page at the same positions leave those positions unspecified.  dtype: MOE_BF16, MOE_F16
+ * or MOE_F32. */
+MOE_API int moe_kv_store(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *cu_dev,
+                         const int32_t *start_dev, const moe_rows *k, const moe_rows *v, int32_t n_tokens,
+                         int32_t dtype, void *stream);
+
+/* Read rows back as the values they stand for (rounded once to dtype): the inverse
+ * addressing of moe_kv_store, k and v are written.  Padding rows are left as they were. */
+MOE_API int moe_kv_load(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *cu_dev,
+                        const int32_t *start_dev, const moe_rows *k, const moe_rows *v, int32_t n_tokens,
+                        int32_t dtype, void *stream);
+
+/* Attention of one token per sequence over its cached positions:
+ *   z_j = scale * q . k_j,  p = softmax(z) over j < len_dev[b],  out = sum_j p_j v_j,
+ * for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  q and out are
+ * [n_seqs][n_q_heads][head_dim], dtype MOE_BF16 or MOE_F16, and may be the same memory
+ * only when they do not overlap.  len_dev: n_seqs int32, 0 <= len <= max_len (an upper
+ * bound that the host knows; it sizes the launch); a sequence of length 0 gets zeros.  With
+ * score, the weights are added to it: score[b][h][j] += sum of p_j over the query heads of
+ * KV head h, j < len; entries from len on are not touched.  Softmax statistics and sums
+ * are fp32; the cached values are rounded to fp16 (q - 8) * d and the weights to fp16.
+ * workspace: 16-byte aligned device memory of at least moe_kv_attend_workspace bytes,
+ * contents irrelevant; calls that may overlap need one each.  Results do not depend on
+ * the run: no atomics. */
+MOE_API int moe_kv_attend(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *len_dev,
+                          int32_t max_len, const moe_rows *q, int32_t n_q_heads, int32_t dtype, float scale,
+                          const moe_rows *out, const moe_kv_score *score, void *workspace,
+                          size_t workspace_bytes, void *stream);
+MOE_API int moe_kv_attend_workspace(const moe_kv_pool *cache, const moe_kv_table *table, int32_t n_q_heads,
+                                    int32_t max_len, int32_t scored, size_t *bytes);
+
+/* Cut sequences down to keep positions by their accumulated weights (the expert cache's
+ * calibrated placement, for attention): per sequence and KV head, the last `recent`
+ * positions and the keep - recent of the others with the largest score stay (ties -> lower
+ * position, NaN below everything); a sequence of length <= keep stays whole.  The kept
+ * rows are copied in order to positions 0 .. of the pages that out_table names in the same
+ * pool, which must not be pages that table names; their scores go to out_score_dev
+ * ([n_seqs][n_kv_heads][keep] fp32, NULL = not wanted, 0 behind the end), their former
+ * positions to kept_dev ([n_seqs][n_kv_heads][keep] int32, -1 behind the end), the new
+ * lengths to out_len_dev ([n_seqs]).  The old pages are not changed, so pages shared with
+ * other sequences stay good.  Destination rows behind the new length are left as they
+ * were.  out_len_dev and out_score_dev may not be the arrays that are read. */
+MOE_API int moe_kv_evict(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *len_dev,
+                         int32_t max_len, const moe_kv_score *score, int32_t keep, int32_t recent,
+                         const moe_kv_table *out_table, int32_t *out_len_dev, int32_t *kept_dev,
+                         float *out_score_dev, void *stream);
 
 /* Free everything.  NULL is a no-op. */
 MOE_API void moe_destroy(moe_ctx *ctx);
