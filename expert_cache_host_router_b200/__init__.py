@@ -143,6 +143,8 @@ _SIGS = {
     "moe_kv_evict": (ctypes.c_int, [ctypes.POINTER(KvPool), ctypes.POINTER(KvTable), _P, ctypes.c_int32,
                                     ctypes.POINTER(KvScore), ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(KvTable),
                                     _P, _P, _P, _P]),
+    "moe_attend_prompt": (ctypes.c_int, [ctypes.c_int32] + [ctypes.POINTER(Rows)] * 4 + [_P] + [ctypes.c_int32] * 6
+                          + [ctypes.c_float, _P, _P]),
     "moe_destroy": (None, [_P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -467,6 +469,7 @@ def _on(stream, dev):
     """The stream to launch on and, for buffers allocated here, the context that ties them to it."""
     import contextlib
     import torch
+    _need(dev.type == "cuda", f"the tensors are on {dev}, not on a CUDA device")
     if stream is None:
         return torch.cuda.current_stream(dev).cuda_stream, contextlib.nullcontext()
     _need(stream.device == dev, f"the stream is on {stream.device}, the tensors are on {dev}")
@@ -597,3 +600,32 @@ def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out
         _check(lib().moe_kv_evict(c, t, lens_p, max_len, sc, keep, recent, o, out_lens.data_ptr(), kept.data_ptr(),
                                   out_score.data_ptr(), s), "moe_kv_evict")
     return out_lens, kept, out_score
+
+
+def attend_prompt(q, k, v, cu, scale=None, out=None, error=None, stream=None):
+    """Causal attention of packed prompts: q [tokens, query heads, head dim], k and v [tokens,
+    KV heads, head dim] (bf16 or fp16), sequence b being rows cu[b] .. cu[b + 1] - 1 (cu: int32
+    [sequences + 1]).  scale: default head_dim ** -0.5.  Returns out (q's shape and type);
+    rows outside every sequence are left as they were (unspecified in a tensor made here).
+    error: int32 [1], MOE_DEVERR_PAGE when a sequence's bounds are outside the rows."""
+    import torch
+    dev = q.device
+    _need(q.is_cuda and q.dim() == 3 and k.dim() == 3, "attend_prompt: q, k and v must be CUDA tensors of three dimensions")
+    n, heads, dim = q.shape
+    kv = k.shape[1]
+    rq = _rows(q, n, heads, dim, q.dtype, dev, "attend_prompt: q")
+    rk = _rows(k, n, kv, dim, q.dtype, dev, "attend_prompt: k")
+    rv = _rows(v, n, kv, dim, q.dtype, dev, "attend_prompt: v")
+    cu_p = _ints(cu, 1, dev, "attend_prompt: cu")
+    _need(cu.shape[0] >= 1, "attend_prompt: cu is empty")
+    err = None if error is None else _ints(error, 1, dev, "attend_prompt: error")
+    s, ctx = _on(stream, dev)
+    if out is None:
+        with ctx:
+            out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+    ro = _rows(out, n, heads, dim, q.dtype, dev, "attend_prompt: out")
+    if n:
+        _check(lib().moe_attend_prompt(dev.index, rq, rk, rv, ro, cu_p, cu.shape[0] - 1, n, heads, kv, dim,
+                                       _dtype(q.dtype, "attend_prompt"), dim ** -0.5 if scale is None else scale, err, s),
+               "moe_attend_prompt")
+    return out

@@ -1,0 +1,551 @@
+// attend_prompt.cu -- causal attention of whole prompts for libmoe: grouped heads, sequences
+// of different lengths packed into one call, on the 5th-generation tensor cores.
+//
+//   o_i = sum_{j <= i} p_ij v_j,  p_i = softmax_j(scale q_i . k_j)   inside each sequence
+//
+// Two products per key tile, S = Q K^T and O += P V, 4 D FLOP per (row, key) pair, bound by
+// the tensor rate for long prompts; one exponential per pair is the next bound: a CTA's 256
+// rows x 128 keys take 2048 cycles of tensor pipe (D = 128) and 2048 cycles of the
+// exponential unit (16 per cycle and SM), so both have to run at the same time.
+//
+// One CTA takes 256 query rows of one head as two tiles of 128, whose softmax and products
+// alternate: while one tile's weights are formed by four warps, the tensor pipe works for
+// the other.  Warp roles, joined by mbarriers:
+//   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns a row; it reads S from tensor
+//                     memory, keeps the row's maximum and sum in registers, writes P (16-bit)
+//                     over S, and rescales O in tensor memory when the maximum has grown
+//   warp 8            TMA of Q, then of K and V tiles (128 keys) into a ring
+//   warp 9            tcgen05.mma: S from shared memory, O with P from tensor memory
+// Tensor memory: S0, S1 (128 columns each; P takes the first 64 of its S), O0, O1 (D each).
+// The maximum that a row's exponents refer to moves only when it is exceeded by more than
+// 2^8, so most key tiles rescale nothing; P stays below 256, inside either 16-bit type.
+// P is rounded to the input type (half a step per weight); sums, S and O are fp32.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "kv_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kPM = 128;      // query rows of a tile
+constexpr int kPN = 128;      // keys of a tile
+constexpr int kPThreads = 320;
+
+struct PromptArgs {
+  const int32_t* cu;
+  int n_seqs, n_tokens, n_heads, group, n_blocks;
+  float scale2;  // scale * log2(e)
+  void* out;
+  int64_t o_tok, o_head;
+  int vec;
+  int32_t* error;
+};
+
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(kv_smem(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(kv_smem(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// False after about 2 s, or at once when another role gave up.
+__device__ __noinline__ bool bar_spin(uint64_t* b, uint32_t parity, volatile int* abort) {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  while (!bar_try(b, parity)) {
+    if (*abort) return false;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > 2000000000ull) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+  return bar_try(b, parity) || bar_spin(b, parity, abort);
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(kv_smem(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(kv_smem(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(kv_smem(b))
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(kv_smem(b)) : "memory");
+}
+
+// Shared-memory operand with 128-byte swizzle.  K-major (Q, K): rows of 64 elements, 8-row
+// groups 1024 bytes apart.  MN-major (V): 64 channels of a key in 128 bytes, 8-key groups
+// 1024 bytes apart (the stride offset), the next 64 channels lbo bytes on (the leading one).
+__device__ __forceinline__ uint64_t op_desc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+#define R8(v, i) v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]
+#define O4(c, v, i) c(v[i]), c(v[i + 1]), c(v[i + 2]), c(v[i + 3])
+#define O32(c, v)                                                                                                   \
+  O4(c, v, 0), O4(c, v, 4), O4(c, v, 8), O4(c, v, 12), O4(c, v, 16), O4(c, v, 20), O4(c, v, 24), O4(c, v, 28)
+#define O16(c, v) O4(c, v, 0), O4(c, v, 4), O4(c, v, 8), O4(c, v, 12)
+__device__ __forceinline__ void tm_ld32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : O32("=r", r)
+      : "r"(at));
+}
+__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::O32("r", r),
+      "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::O16("r", r),
+      "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Uses of loaded registers cannot be scheduled before the wait: they pass through here after it.
+__device__ __forceinline__ void tm_landed32(uint32_t* r) { asm volatile("" : O32("+r", r)); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D>
+struct PromptSmem {
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr uint32_t kBox = 128 * 128;             // 128 rows of 64 elements
+  static constexpr uint32_t kTileB = (D / 64) * kBox;     // a Q, K or V tile
+  static constexpr uint32_t kQ = 0, kK = 2 * kTileB, kV = kK + kStages * kTileB, kEnd = kV + kStages * kTileB;
+  static constexpr uint32_t kBars = kEnd, kBytes = kEnd + 512 + 1024;  // + alignment to 1024
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+    attend_prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mv) {
+  using S = PromptSmem<D>;
+  constexpr int ST = S::kStages, NB = D / 64;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (kv_smem(raw) & 1023u)) & 1023u);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + S::kBars);
+  uint64_t *s_full = q_full + 2, *p_full = q_full + 4, *o_done = q_full + 6, *fix = q_full + 8;
+  uint64_t *k_full = q_full + 9, *k_empty = k_full + ST, *v_full = k_empty + ST, *v_empty = v_full + ST;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(v_empty + ST);
+  int* found = reinterpret_cast<int*>(tmem_at + 1);  // sequence's first row, rows, block
+  volatile int* abort = found + 3;
+  int* wsum = found + 4;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // Which sequence and block: blocks are numbered along the sequences, the last first (the
+  // longest rows of a sequence start first), heads of a block side by side.
+  const int head = blockIdx.x % a.n_heads, blk = a.n_blocks - 1 - blockIdx.x / a.n_heads;
+  if (tid == 0) {
+    found[0] = -1;
+    *abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      bar_init(q_full + i, 1);
+      bar_init(s_full + i, 1);
+      bar_init(p_full + i, 4);
+      bar_init(o_done + i, 1);
+    }
+    bar_init(fix, 1);
+    for (int i = 0; i < ST; ++i) {
+      bar_init(k_full + i, 1);
+      bar_init(k_empty + i, 1);
+      bar_init(v_full + i, 1);
+      bar_init(v_empty + i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  int carry = 0;
+  for (int base = 0; base < a.n_seqs; base += kPThreads) {
+    const int b = base + tid;
+    int s = 0, e = 0;
+    if (b < a.n_seqs) {
+      s = a.cu[b];
+      e = a.cu[b + 1];
+      if (s < 0 || e < s || e > a.n_tokens) {
+        kv_flag(a.error, MOE_DEVERR_PAGE);
+        e = s;
+      }
+    }
+    const int mine = (e - s + 2 * kPM - 1) / (2 * kPM);
+    int v = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += y;
+    }
+    __syncthreads();
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    int sum = carry;
+    for (int w = 0; w < kPThreads / 32; ++w) {
+      if (w < warp) sum += wsum[w];
+      carry += wsum[w];
+    }
+    const int first = sum + v - mine;
+    if (blk >= first && blk < first + mine) {
+      found[0] = s;
+      found[1] = e - s;
+      found[2] = blk - first;
+    }
+  }
+  __syncthreads();
+  const int row0 = found[0], n = found[1], qb = found[2];
+  if (row0 < 0) return;  // the grid is an upper bound
+
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(kv_smem(tmem_at)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_at;
+  // key tiles of the two query tiles
+  const int kv_tiles = (n + kPN - 1) / kPN;
+  const int n0 = 2 * qb + 1, n1 = 2 * qb + 2 <= kv_tiles ? 2 * qb + 2 : 0;
+  const int n_kv = n1 ? n1 : n0;
+  const uint32_t qa = kv_smem(sm + S::kQ), ka = kv_smem(sm + S::kK), va = kv_smem(sm + S::kV);
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int nt = w ? n1 : n0;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t st = tmem + lanes + w * 128, ot = tmem + lanes + 256 + w * D;
+    float m = -INFINITY, l = 0.0f;  // m in units of S
+    bool ok = true;
+    for (int j = 0; j < nt && ok; ++j) {
+      ok = __all_sync(0xffffffffu, bar_wait(s_full + w, j & 1, abort));
+      if (!ok) break;
+      tc_after();
+      uint32_t s[128];
+      float* f = reinterpret_cast<float*>(s);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tm_ld32(st + 32 * c, s + 32 * c);
+      tm_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tm_landed32(s + 32 * c);
+      if (j == nt - 1) {  // the diagonal tile: keys behind the row (and so behind the sequence)
+#pragma unroll
+        for (int c = 0; c < 128; ++c) f[c] = c > row ? -INFINITY : f[c];
+      }
+      float mx[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+      for (int c = 4; c < 128; c += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], f[c + i]);
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool grow = (top - m) * a.scale2 > 8.0f || m == -INFINITY;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = fmaxf(m, top);
+        const float al = m == mn ? 1.0f : ex2((m - mn) * a.scale2);
+        m = mn;
+        l *= al;
+        if (j > 0) {
+          ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (j - 1) & 1, abort));
+          if (!ok) break;
+          tc_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tm_ld32(ot + c, o);
+            tm_wait_ld();
+            tm_landed32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tm_st32(ot + c, o);
+          }
+        }
+      }
+      const float off = -m * a.scale2;
+      float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float x = ex2(fmaf(f[c + i], a.scale2, off)), y = ex2(fmaf(f[c + i + 1], a.scale2, off));
+          sum[i & 2] += x;
+          sum[(i & 2) + 1] += y;
+          p[i >> 1] = pack2<T>(x, y);
+        }
+        tm_st16(st + c / 2, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tm_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(p_full + w);
+    }
+    if (nt > 0) {
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (nt - 1) & 1, abort));
+      tc_after();
+      const int r = qb * 2 * kPM + w * kPM + row;
+      const float inv = ok ? 1.0f / l : __int_as_float(0x7fc00000);
+      if (!ok && lane == 0) kv_flag(a.error, MOE_DEVERR_TMA);
+      T* dst = static_cast<T*>(a.out) + (int64_t)(row0 + r) * a.o_tok + head * a.o_head;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tm_ld32(ot + c, o);
+        tm_wait_ld();
+        tm_landed32(o);
+        if (r < n) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          if (a.vec) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) reinterpret_cast<uint16_t*>(dst + c)[i] = (uint16_t)(p[i >> 1] >> (16 * (i & 1)));
+          }
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- TMA
+    const int kh = head / a.group;
+    if (lane == 0) {
+      for (int w = 0; w < (n1 ? 2 : 1); ++w) {
+        bar_expect(q_full + w, S::kTileB);
+        for (int c = 0; c < NB; ++c)
+          tma3(qa + w * S::kTileB + c * S::kBox, &mq, 64 * c, head, row0 + qb * 2 * kPM + w * kPM, q_full + w);
+      }
+    }
+    for (int j = 0; j < n_kv; ++j) {
+      const int s = j % ST, it = j / ST;
+      bool ok = true;
+      if (it) ok = bar_wait(k_empty + s, (it - 1) & 1, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        bar_expect(k_full + s, S::kTileB);
+        for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, row0 + j * kPN, k_full + s);
+      }
+      if (it) ok = bar_wait(v_empty + s, (it - 1) & 1, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int left = n - j * kPN;  // keys of this tile that are the sequence's
+      uint64_t* vb = left < kPN ? fix : v_full + s;
+      if (lane == 0) {
+        bar_expect(vb, S::kTileB);
+        for (int c = 0; c < NB; ++c) tma3(va + s * S::kTileB + c * S::kBox, &mv, 64 * c, kh, row0 + j * kPN, vb);
+      }
+      if (left < kPN) {
+        // Values behind the sequence (another one's, perhaps not finite) meet weights of 0:
+        // they are cleared before the product sees them.
+        if (!__all_sync(0xffffffffu, bar_wait(fix, 0, abort))) break;
+        for (int i = lane; i < (kPN - left) * NB * 8; i += 32) {
+          const int r = left + i / (NB * 8), c = (i / 8) % NB;
+          *reinterpret_cast<uint4*>(sm + S::kV + s * S::kTileB + c * S::kBox + r * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(v_full + s);
+      }
+    }
+  } else if (lane == 0) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t ty = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    constexpr uint32_t base = (1u << 4) | (ty << 7) | (ty << 10) | ((uint32_t)(kPM >> 4) << 24);
+    constexpr uint32_t id_s = base | ((uint32_t)(kPN >> 3) << 17);
+    constexpr uint32_t id_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
+    auto s_mma = [&](int w, int j) {
+      const uint32_t q = qa + w * S::kTileB, k = ka + (j % ST) * S::kTileB;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * S::kBox + (kk & 3) * 32;
+        mma_ss(tmem + w * 128, op_desc(q + o, 16), op_desc(k + o, 16), id_s, kk > 0);
+      }
+      commit(s_full + w);
+    };
+    auto o_mma = [&](int w, int j) {
+      const uint32_t v = va + (j % ST) * S::kTileB;
+#pragma unroll
+      for (int kk = 0; kk < kPN / 16; ++kk)
+        mma_ts(tmem + 256 + w * D, tmem + w * 128 + kk * 8, op_desc(v + kk * 2048, S::kBox), id_o, j > 0 || kk > 0);
+      commit(o_done + w);
+    };
+    bool ok = bar_wait(k_full, 0, abort) && bar_wait(q_full, 0, abort);
+    if (ok) {
+      tc_after();
+      s_mma(0, 0);
+      if (n1) {
+        ok = bar_wait(q_full + 1, 0, abort);
+        if (ok) s_mma(1, 0);
+      }
+      commit(k_empty);
+    }
+    for (int j = 0; j < n_kv && ok; ++j) {
+      ok = bar_wait(v_full + j % ST, (j / ST) & 1, abort);
+      for (int w = 0; w < 2 && ok; ++w) {
+        const int nt = w ? n1 : n0;
+        if (j < nt) {
+          ok = bar_wait(p_full + w, j & 1, abort);
+          if (!ok) break;
+          tc_after();
+          o_mma(w, j);
+        }
+        if (j + 1 < nt) {
+          ok = bar_wait(k_full + (j + 1) % ST, ((j + 1) / ST) & 1, abort);
+          if (!ok) break;
+          tc_after();
+          s_mma(w, j + 1);
+        }
+      }
+      commit(v_empty + j % ST);
+      if (j + 1 < n_kv) commit(k_empty + (j + 1) % ST);
+    }
+  }
+  tc_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// Rows [tokens][heads][D] -> boxes of 128 tokens x 64 channels of one head, 128-byte swizzle.
+bool rows_map(CUtensorMap* m, const moe_rows* r, int tokens, int heads, int dim, int dtype) {
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)r->head_stride * 2, (cuuint64_t)r->token_stride * 2};
+  const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+  return encode_tiled()(m, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        r->data_dev, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t prompt_go(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int device,
+                      cudaStream_t st) {
+  static bool ready[kKvMaxDevices];
+  if (!ready[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               PromptSmem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    ready[device] = true;
+  }
+  attend_prompt_kernel<T, D><<<a.n_blocks * a.n_heads, kPThreads, PromptSmem<D>::kBytes, st>>>(a, mq, mk, mv);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_rows* k, const moe_rows* v, const moe_rows* out,
+                                 const int32_t* cu_dev, int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads,
+                                 int32_t n_kv_heads, int32_t head_dim, int32_t dtype, float scale, int32_t* error_dev,
+                                 void* stream) {
+  if (!q || !k || !v || !out || !cu_dev || !q->data_dev || !k->data_dev || !v->data_dev || !out->data_dev) return MOE_ERR_INVALID;
+  if (device < 0 || device >= kKvMaxDevices || n_seqs < 0 || n_tokens < 0 || n_q_heads < 1 || n_kv_heads < 1 ||
+      n_q_heads % n_kv_heads)
+    return MOE_ERR_INVALID;
+  if ((dtype != MOE_BF16 && dtype != MOE_F16) || !(scale > 0.0f) || scale - scale != 0.0f) return MOE_ERR_INVALID;
+  if (!kv_dim_ok(head_dim) || n_seqs > kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
+  for (const moe_rows* r : {q, k, v}) {  // the TMA's rules
+    if (!kv_align_ok(r->data_dev, 16) || r->token_stride % 8 || r->head_stride % 8) return MOE_ERR_UNSUPPORTED;
+    if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride >= (1ll << 38) || r->head_stride >= (1ll << 38))
+      return MOE_ERR_UNSUPPORTED;
+  }
+  if (!kv_align_ok(out->data_dev, 2)) return MOE_ERR_INVALID;
+  if (n_tokens == 0 || n_seqs == 0) return MOE_OK;
+  const int64_t blocks = n_tokens / (2 * kPM) + (n_seqs < n_tokens ? n_seqs : n_tokens);
+  if (blocks * n_q_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  DeviceScope dev(device);
+  if (!dev.ok) return MOE_ERR_CUDA;
+  if (!encode_tiled()) return MOE_ERR_UNSUPPORTED;
+  CUtensorMap mq, mk, mv;
+  if (!rows_map(&mq, q, n_tokens, n_q_heads, head_dim, dtype) || !rows_map(&mk, k, n_tokens, n_kv_heads, head_dim, dtype) ||
+      !rows_map(&mv, v, n_tokens, n_kv_heads, head_dim, dtype))
+    return MOE_ERR_UNSUPPORTED;
+  PromptArgs a{};
+  a.cu = cu_dev;
+  a.n_seqs = n_seqs;
+  a.n_tokens = n_tokens;
+  a.n_heads = n_q_heads;
+  a.group = n_q_heads / n_kv_heads;
+  a.n_blocks = (int)blocks;
+  a.scale2 = scale * 1.4426950408889634f;
+  a.out = out->data_dev;
+  a.o_tok = out->token_stride;
+  a.o_head = out->head_stride;
+  a.vec = kv_align_ok(out->data_dev, 16) && out->token_stride % 8 == 0 && out->head_stride % 8 == 0;
+  a.error = error_dev;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == MOE_BF16)
+    e = head_dim == 64 ? prompt_go<__nv_bfloat16, 64>(a, mq, mk, mv, device, st) : prompt_go<__nv_bfloat16, 128>(a, mq, mk, mv, device, st);
+  else
+    e = head_dim == 64 ? prompt_go<__half, 64>(a, mq, mk, mv, device, st) : prompt_go<__half, 128>(a, mq, mk, mv, device, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -811,7 +811,8 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   int bad = kv_check(cache, table, &c);
   if (bad) return bad;
   if (!len_dev || !q || !out || !q->data_dev || !out->data_dev || (score && !score->data_dev)) return MOE_ERR_INVALID;
-  if ((dtype != MOE_BF16 && dtype != MOE_F16) || !(scale - scale == 0.0f)) return MOE_ERR_INVALID;
+  if ((dtype != MOE_BF16 && dtype != MOE_F16) || !(scale > 0.0f) || scale - scale != 0.0f)
+    return MOE_ERR_INVALID;
   if (!kv_align_ok(q->data_dev, 2) || !kv_align_ok(out->data_dev, 2)) return MOE_ERR_INVALID;
   bad = attend_plan(c, cache->device, n_q_heads, max_len, score != nullptr, &p);
   if (bad) return bad;

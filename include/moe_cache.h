@@ -429,9 +429,9 @@ MOE_API int moe_kv_load(const moe_kv_pool *cache, const moe_kv_table *table, con
 
 /* Attention of one token per sequence over its cached positions:
  *   z_j = scale * q . k_j,  p = softmax(z) over j < len_dev[b],  out = sum_j p_j v_j,
- * for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  q and out are
- * [n_seqs][n_q_heads][head_dim], dtype MOE_BF16 or MOE_F16, and may be the same memory
- * only when they do not overlap.  len_dev: n_seqs int32, 0 <= len <= max_len (an upper
+ * scale > 0, for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  q and out are
+ * [n_seqs][n_q_heads][head_dim], dtype MOE_BF16 or MOE_F16, and may not overlap.
+ * len_dev: n_seqs int32, 0 <= len <= max_len (an upper
  * bound that the host knows; it sizes the launch); a sequence of length 0 gets zeros.  With
  * score, the weights are added to it: score[b][h][j] += sum of p_j over the query heads of
  * KV head h, j < len; entries from len on are not touched.  Softmax statistics and sums
@@ -461,6 +461,22 @@ MOE_API int moe_kv_evict(const moe_kv_pool *cache, const moe_kv_table *table, co
                          int32_t max_len, const moe_kv_score *score, int32_t keep, int32_t recent,
                          const moe_kv_table *out_table, int32_t *out_len_dev, int32_t *kept_dev,
                          float *out_score_dev, void *stream);
+
+/* Causal attention of whole prompts, packed into one call: sequence b is rows cu_dev[b] ..
+ * cu_dev[b + 1] - 1 of q, k, v and out (cu_dev: n_seqs + 1 int32, ascending);
+ *   out_i = sum over j <= i of the same sequence of p_ij v_j,  p_i = softmax_j(scale * q_i . k_j).
+ * q and out are [n_tokens][n_q_heads][head_dim], k and v [n_tokens][n_kv_heads][head_dim]
+ * (query head h reads KV head h / (n_q_heads / n_kv_heads)); head_dim 64 or 128, dtype
+ * MOE_BF16 or MOE_F16; q, k and v 16-byte aligned with strides that are multiples of 8
+ * elements.  out may not overlap q, k or v.  scale > 0.  Rows outside every sequence are left as they were.
+ * Products and sums are fp32, the weights are rounded to dtype.  A value row that is not
+ * finite makes rows of its own sequence from its tile of 128 positions on NaN, also those
+ * before it in that tile; never rows of another sequence.  A sequence whose bounds are not
+ * 0 <= cu[b] <= cu[b + 1] <= n_tokens is skipped and sets error_dev (may be NULL). */
+MOE_API int moe_attend_prompt(int32_t device, const moe_rows *q, const moe_rows *k, const moe_rows *v,
+                              const moe_rows *out, const int32_t *cu_dev, int32_t n_seqs, int32_t n_tokens,
+                              int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t dtype, float scale,
+                              int32_t *error_dev, void *stream);
 
 /* Free everything.  NULL is a no-op. */
 MOE_API void moe_destroy(moe_ctx *ctx);
