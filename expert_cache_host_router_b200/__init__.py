@@ -414,92 +414,112 @@ class ExpertCacheMoE:
 
 
 # ------------------------------------------------------------------ attention operators
+#
+# These calls are made once per layer and token, so the checks below build their messages
+# only when they fail.
 
-_DTYPES = {"torch.bfloat16": MOE_BF16, "torch.float16": MOE_F16, "torch.float32": MOE_F32}
-
-
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise MoEError(MOE_ERR_INVALID, what)
-
-
-def _dtype(t, what: str) -> int:
-    d = _DTYPES.get(str(t))
-    _need(d is not None, f"{what}: dtype {t}")
-    return d
+_torch = None  # torch, imported by the first call; with it _DT and the types the checks compare with
+_DT = {}
 
 
-def _ints(t, dim: int, dev, what: str) -> int:
+def _load_torch():
+    global _torch
     import torch
-    _need(t.dtype == torch.int32 and t.dim() == dim and t.device == dev and (t.shape[-1] <= 1 or t.stride(-1) == 1),
-          f"{what} must be an int32 tensor of {dim} dimension(s) on {dev}, its last one contiguous")
+    _DT.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32})
+    _torch = torch
+    return torch
+
+
+def _refuse(what: str):
+    raise MoEError(MOE_ERR_INVALID, what)
+
+
+def _ints(t, dim: int, dev, what: str, n=None) -> int:
+    if t.dtype != _torch.int32 or t.dim() != dim or t.device != dev or (n is not None and t.shape[0] != n) \
+            or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        _refuse(f"{what} must be an int32 tensor of {dim} dimension(s){'' if n is None else f' and {n} entries'} on {dev}, "
+                "its last one contiguous")
     return t.data_ptr()
 
 
 def _kv_pool(pool, error, what: str):
-    import torch
-    _need(pool.dtype == torch.uint8 and pool.dim() == 4 and pool.is_cuda and pool.is_contiguous(),
-          f"{what}: pool must be a contiguous uint8 CUDA tensor [pages, KV heads, page tokens / 16, 18 * head dim]")
+    if _torch is None:
+        _load_torch()
+    if pool.dtype != _torch.uint8 or pool.dim() != 4 or not pool.is_cuda or not pool.is_contiguous() or pool.shape[3] % 18:
+        _refuse(f"{what}: pool must be a contiguous uint8 CUDA tensor [pages, KV heads, page tokens / 16, 18 * head dim]")
     pages, heads, tiles, size = pool.shape
-    _need(size % 18 == 0, f"{what}: pool tiles must have 18 * head dim bytes")
-    err = None if error is None else _ints(error, 1, pool.device, f"{what}: error")
-    return KvPool(pool.data_ptr(), pages, heads, size // 18, tiles * 16, pool.device.index, err)
+    dev = pool.device
+    return dev, KvPool(pool.data_ptr(), pages, heads, size // 18, tiles * 16, dev.index,
+                       None if error is None else _ints(error, 1, dev, what + ": error"))
 
 
 def _kv_table(table, dev, what: str):
-    p = _ints(table, 2, dev, f"{what}: table")
-    return KvTable(p, table.shape[0], table.shape[1], table.stride(0) if table.shape[0] > 1 else table.shape[1])
+    p = _ints(table, 2, dev, what)
+    n, w = table.shape
+    return KvTable(p, n, w, table.stride(0) if n > 1 else w)
 
 
 def _rows(t, n, heads, dim, dtype, dev, what: str):
-    _need(tuple(t.shape) == (n, heads, dim) and t.dtype == dtype and t.device == dev and t.stride(2) == 1,
-          f"{what} must be a {dtype} tensor {[n, heads, dim]} on {dev}, its last dimension contiguous")
+    if t.shape != (n, heads, dim) or t.dtype != dtype or t.device != dev or t.stride(2) != 1:
+        _refuse(f"{what} must be a {dtype} tensor {[n, heads, dim]} on {dev}, its last dimension contiguous")
     return Rows(t.data_ptr(), t.stride(0), t.stride(1))
 
 
 def _kv_score(score, n, heads, most, dev, what: str):
-    import torch
-    _need(score.dtype == torch.float32 and score.dim() == 3 and tuple(score.shape[:2]) == (n, heads)
-          and score.shape[2] >= most and score.device == dev and (score.shape[2] <= 1 or score.stride(2) == 1),
-          f"{what}: score must be a float32 tensor [{n}, {heads}, >= {most}] on {dev}, its last dimension contiguous")
+    if score.dtype != _torch.float32 or score.dim() != 3 or score.shape[0] != n or score.shape[1] != heads \
+            or score.shape[2] < most or score.device != dev or (score.shape[2] > 1 and score.stride(2) != 1):
+        _refuse(f"{what} must be a float32 tensor [{n}, {heads}, >= {most}] on {dev}, its last dimension contiguous")
     return KvScore(score.data_ptr(), score.stride(0), score.stride(1))
 
 
-def _on(stream, dev):
-    """The stream to launch on and, for buffers allocated here, the context that ties them to it."""
-    import contextlib
-    import torch
-    _need(dev.type == "cuda", f"the tensors are on {dev}, not on a CUDA device")
+def _dtype(t, what: str) -> int:
+    d = _DT.get(t)
+    return _refuse(f"{what}: dtype {t}") if d is None else d
+
+
+def _stream(stream, dev) -> int:
+    """Handle of the stream to launch on (the current one of the tensors' device without `stream`)."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream, contextlib.nullcontext()
-    _need(stream.device == dev, f"the stream is on {stream.device}, the tensors are on {dev}")
-    return stream.cuda_stream, torch.cuda.stream(stream)
+        return _torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        _refuse(f"the stream is on {stream.device}, the tensors are on {dev}")
+    return stream.cuda_stream
+
+
+def _empty(stream, shape, dtype, dev):
+    """A buffer that belongs to the stream that the call runs on."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=dev)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=dev)
 
 
 def kv_pool(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device=0):
     """A zeroed 4-bit key/value cache: uint8 [n_pages, n_kv_heads, page_tokens / 16, 18 * head_dim]
     (page_tokens a multiple of 16, head_dim 64 or 128; layout in include/moe_cache.h)."""
-    import torch
-    _need(page_tokens > 0 and page_tokens % 16 == 0, f"kv_pool: page_tokens {page_tokens} is not a multiple of 16")
-    _need(head_dim in (64, 128), f"kv_pool: head_dim {head_dim} is neither 64 nor 128")
+    torch = _torch or _load_torch()
+    if page_tokens < 16 or page_tokens % 16:
+        _refuse(f"kv_pool: page_tokens {page_tokens} is not a multiple of 16")
+    if head_dim not in (64, 128):
+        _refuse(f"kv_pool: head_dim {head_dim} is neither 64 nor 128")
     return torch.zeros((n_pages, n_kv_heads, page_tokens // 16, 18 * head_dim), dtype=torch.uint8,
                        device=torch.device("cuda", device) if isinstance(device, int) else device)
 
 
-def _kv_rows_call(name, pool, k, v, table, cu, start, n, stream_ptr, error):
-    dev = pool.device
-    c = _kv_pool(pool, error, name)
-    t = _kv_table(table, dev, name)
-    cu_p = _ints(cu, 1, dev, f"{name}: cu")
-    _need(cu.shape[0] == t.n_seqs + 1, f"{name}: cu must have {t.n_seqs + 1} entries")
-    start_p = None
-    if start is not None:
-        start_p = _ints(start, 1, dev, f"{name}: start")
-        _need(start.shape[0] == t.n_seqs, f"{name}: start must have {t.n_seqs} entries")
-    rk = _rows(k, n, c.n_kv_heads, c.head_dim, k.dtype, dev, f"{name}: k")
-    rv = _rows(v, n, c.n_kv_heads, c.head_dim, k.dtype, dev, f"{name}: v")
-    if n:
-        _check(getattr(lib(), "moe_" + name)(c, t, cu_p, start_p, rk, rv, n, _dtype(k.dtype, name), stream_ptr), "moe_" + name)
+def _kv_rows_call(call, name, pool, k, v, table, cu, start, n, stream, error):
+    dev, c = _kv_pool(pool, error, name)
+    t = _kv_table(table, dev, name + ": table")
+    b, heads, dim, dt = t.n_seqs, c.n_kv_heads, c.head_dim, k.dtype
+    cu_p = _ints(cu, 1, dev, name + ": cu", b + 1)
+    start_p = None if start is None else _ints(start, 1, dev, name + ": start", b)
+    rk = _rows(k, n, heads, dim, dt, dev, name + ": k")
+    rv = _rows(v, n, heads, dim, dt, dev, name + ": v")
+    d = _dtype(dt, name)
+    s = _stream(stream, dev)
+    if n and b:
+        st = call(c, t, cu_p, start_p, rk, rv, n, d, s)
+        if st:
+            raise MoEError(st, "moe_" + name)
 
 
 def kv_store(pool, k, v, table, cu, start=None, error=None, stream=None) -> None:
@@ -507,22 +527,20 @@ def kv_store(pool, k, v, table, cu, start=None, error=None, stream=None) -> None
     rows cu[b] .. cu[b + 1] - 1 go to positions start[b] .. (0 .. without start) of sequence
     b, whose pages are table[b].  Rows outside cu[0] .. cu[-1] are padding.  error: int32
     [1], receives MOE_DEVERR_PAGE when a row has no place in the cache (that row is skipped)."""
-    s, _ = _on(stream, pool.device)
-    _kv_rows_call("kv_store", pool, k, v, table, cu, start, k.shape[0], s, error)
+    _kv_rows_call(lib().moe_kv_store, "kv_store", pool, k, v, table, cu, start, k.shape[0], stream, error)
 
 
 def kv_load(pool, table, cu, start, n_tokens: int, dtype, out=None, error=None, stream=None):
     """Read cached rows back as the values they stand for, addressed as in kv_store.  Returns
     (k, v) [n_tokens, KV heads, head dim]; out: that pair of tensors to write to.  Padding
     rows are left as they were (unspecified in tensors made here)."""
-    import torch
-    s, ctx = _on(stream, pool.device)
     if out is None:
-        shape = (n_tokens, pool.shape[1], pool.shape[3] // 18)
-        with ctx:
-            out = torch.empty(shape, dtype=dtype, device=pool.device), torch.empty(shape, dtype=dtype, device=pool.device)
-    _need(out[0].dtype == dtype, f"kv_load: out must be {dtype}")
-    _kv_rows_call("kv_load", pool, out[0], out[1], table, cu, start, n_tokens, s, error)
+        dev, c = _kv_pool(pool, None, "kv_load")
+        shape = (n_tokens, c.n_kv_heads, c.head_dim)
+        out = _empty(stream, shape, dtype, dev), _empty(stream, shape, dtype, dev)
+    elif out[0].dtype != dtype:
+        _refuse(f"kv_load: out must be {dtype}")
+    _kv_rows_call(lib().moe_kv_load, "kv_load", pool, out[0], out[1], table, cu, start, n_tokens, stream, error)
     return out
 
 
@@ -545,36 +563,40 @@ def kv_attend(pool, q, table, lens, max_len=None, scale=None, score=None, out=No
     kv_attend_workspace(...) bytes for callers that keep their own; made here otherwise.
     Returns out (q's shape and type); a sequence of length 0 gives zeros, one whose length
     or pages lie outside the cache NaN (and error, int32 [1], MOE_DEVERR_PAGE)."""
-    import torch
-    dev = pool.device
-    c = _kv_pool(pool, error, "kv_attend")
-    t = _kv_table(table, dev, "kv_attend")
-    lens_p = _ints(lens, 1, dev, "kv_attend: lens")
-    _need(lens.shape[0] == t.n_seqs and q.dim() == 3, f"kv_attend: lens must have {t.n_seqs} entries, q three dimensions")
-    n, heads, dim = t.n_seqs, q.shape[1], c.head_dim
-    most = t.width * c.page_tokens if max_len is None else int(max_len)
-    rq = _rows(q, n, heads, dim, q.dtype, dev, "kv_attend: q")
-    sc = None if score is None else _kv_score(score, n, c.n_kv_heads, most, dev, "kv_attend")
-    s, ctx = _on(stream, dev)
-    need = _attend_workspace(c.n_kv_heads, dim, c.page_tokens, c.device, n, t.width, heads, most, int(score is not None))
-    with ctx:
-        if out is None:
-            out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _need(workspace.device == dev and workspace.is_contiguous(), f"kv_attend: workspace must be contiguous on {dev}")
-    ro = _rows(out, n, heads, dim, q.dtype, dev, "kv_attend: out")
-    if n:
-        _check(lib().moe_kv_attend(c, t, lens_p, most, rq, heads, _dtype(q.dtype, "kv_attend"),
-                                   dim ** -0.5 if scale is None else scale, ro, sc, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), s), "moe_kv_attend")
+    dev, c = _kv_pool(pool, error, "kv_attend")
+    t = _kv_table(table, dev, "kv_attend: table")
+    n, dim, dt = t.n_seqs, c.head_dim, q.dtype
+    lens_p = _ints(lens, 1, dev, "kv_attend: lens", n)
+    if q.dim() != 3:
+        _refuse("kv_attend: q must have three dimensions")
+    heads = q.shape[1]
+    most = t.width * c.page_tokens if max_len is None else max_len
+    rq = _rows(q, n, heads, dim, dt, dev, "kv_attend: q")
+    sc = None if score is None else _kv_score(score, n, c.n_kv_heads, most, dev, "kv_attend: score")
+    d = _dtype(dt, "kv_attend")
+    s = _stream(stream, dev)
+    if out is None:
+        out = _empty(stream, (n, heads, dim), dt, dev)
+    if not n:
+        return out
+    if workspace is None:
+        workspace = _empty(stream, (_attend_workspace(c.n_kv_heads, dim, c.page_tokens, c.device, n, t.width, heads, most,
+                                                      score is not None),), _torch.uint8, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _refuse(f"kv_attend: workspace must be contiguous on {dev}")
+    ro = _rows(out, n, heads, dim, dt, dev, "kv_attend: out")
+    st = lib().moe_kv_attend(c, t, lens_p, most, rq, heads, d, dim ** -0.5 if scale is None else scale, ro, sc,
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    if st:
+        raise MoEError(st, "moe_kv_attend")
     return out
 
 
 def kv_attend_workspace(pool, table, n_q_heads: int, max_len: int, scored: bool = False) -> int:
     """Bytes of workspace that kv_attend needs for these sizes."""
-    return _attend_workspace(pool.shape[1], pool.shape[3] // 18, pool.shape[2] * 16, pool.device.index, table.shape[0],
-                             table.shape[1], n_q_heads, max_len, int(scored))
+    dev, c = _kv_pool(pool, None, "kv_attend_workspace")
+    return _attend_workspace(c.n_kv_heads, c.head_dim, c.page_tokens, c.device, table.shape[0], table.shape[1], n_q_heads,
+                             max_len, bool(scored))
 
 
 def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out_table, error=None, stream=None):
@@ -583,22 +605,22 @@ def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out
     copied in order to the pages of out_table (pages that table does not name).  Returns
     (lengths int32 [sequences], former positions int32 [sequences, KV heads, keep], scores
     float32 of the same shape); behind a sequence's end positions are -1, scores 0."""
-    import torch
-    dev = pool.device
-    c = _kv_pool(pool, error, "kv_evict")
-    t, o = _kv_table(table, dev, "kv_evict"), _kv_table(out_table, dev, "kv_evict: out_table")
-    lens_p = _ints(lens, 1, dev, "kv_evict: lens")
-    _need(lens.shape[0] == t.n_seqs, f"kv_evict: lens must have {t.n_seqs} entries")
-    sc = _kv_score(score, t.n_seqs, c.n_kv_heads, max_len, dev, "kv_evict")
-    _need(keep >= 1, f"kv_evict: keep {keep}")
-    s, ctx = _on(stream, dev)
-    with ctx:
-        out_lens = torch.empty(t.n_seqs, dtype=torch.int32, device=dev)
-        kept = torch.empty((t.n_seqs, c.n_kv_heads, keep), dtype=torch.int32, device=dev)
-        out_score = torch.empty((t.n_seqs, c.n_kv_heads, keep), dtype=torch.float32, device=dev)
-    if t.n_seqs:
-        _check(lib().moe_kv_evict(c, t, lens_p, max_len, sc, keep, recent, o, out_lens.data_ptr(), kept.data_ptr(),
-                                  out_score.data_ptr(), s), "moe_kv_evict")
+    dev, c = _kv_pool(pool, error, "kv_evict")
+    t, o = _kv_table(table, dev, "kv_evict: table"), _kv_table(out_table, dev, "kv_evict: out_table")
+    n, heads = t.n_seqs, c.n_kv_heads
+    lens_p = _ints(lens, 1, dev, "kv_evict: lens", n)
+    sc = _kv_score(score, n, heads, max_len, dev, "kv_evict: score")
+    if keep < 1:
+        _refuse(f"kv_evict: keep {keep}")
+    s = _stream(stream, dev)
+    out_lens = _empty(stream, (n,), _torch.int32, dev)
+    kept = _empty(stream, (n, heads, keep), _torch.int32, dev)
+    out_score = _empty(stream, (n, heads, keep), _torch.float32, dev)
+    if n:
+        st = lib().moe_kv_evict(c, t, lens_p, max_len, sc, keep, recent, o, out_lens.data_ptr(), kept.data_ptr(),
+                                out_score.data_ptr(), s)
+        if st:
+            raise MoEError(st, "moe_kv_evict")
     return out_lens, kept, out_score
 
 
@@ -608,24 +630,28 @@ def attend_prompt(q, k, v, cu, scale=None, out=None, error=None, stream=None):
     [sequences + 1]).  scale: default head_dim ** -0.5.  Returns out (q's shape and type);
     rows outside every sequence are left as they were (unspecified in a tensor made here).
     error: int32 [1], MOE_DEVERR_PAGE when a sequence's bounds are outside the rows."""
-    import torch
-    dev = q.device
-    _need(q.is_cuda and q.dim() == 3 and k.dim() == 3, "attend_prompt: q, k and v must be CUDA tensors of three dimensions")
+    if _torch is None:
+        _load_torch()
+    if not q.is_cuda or q.dim() != 3 or k.dim() != 3:
+        _refuse("attend_prompt: q, k and v must be CUDA tensors of three dimensions")
+    dev, dt = q.device, q.dtype
     n, heads, dim = q.shape
     kv = k.shape[1]
-    rq = _rows(q, n, heads, dim, q.dtype, dev, "attend_prompt: q")
-    rk = _rows(k, n, kv, dim, q.dtype, dev, "attend_prompt: k")
-    rv = _rows(v, n, kv, dim, q.dtype, dev, "attend_prompt: v")
+    rq = _rows(q, n, heads, dim, dt, dev, "attend_prompt: q")
+    rk = _rows(k, n, kv, dim, dt, dev, "attend_prompt: k")
+    rv = _rows(v, n, kv, dim, dt, dev, "attend_prompt: v")
     cu_p = _ints(cu, 1, dev, "attend_prompt: cu")
-    _need(cu.shape[0] >= 1, "attend_prompt: cu is empty")
+    if cu.shape[0] < 1:
+        _refuse("attend_prompt: cu is empty")
     err = None if error is None else _ints(error, 1, dev, "attend_prompt: error")
-    s, ctx = _on(stream, dev)
+    d = _dtype(dt, "attend_prompt")
+    s = _stream(stream, dev)
     if out is None:
-        with ctx:
-            out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
-    ro = _rows(out, n, heads, dim, q.dtype, dev, "attend_prompt: out")
+        out = _empty(stream, (n, heads, dim), dt, dev)
+    ro = _rows(out, n, heads, dim, dt, dev, "attend_prompt: out")
     if n:
-        _check(lib().moe_attend_prompt(dev.index, rq, rk, rv, ro, cu_p, cu.shape[0] - 1, n, heads, kv, dim,
-                                       _dtype(q.dtype, "attend_prompt"), dim ** -0.5 if scale is None else scale, err, s),
-               "moe_attend_prompt")
+        st = lib().moe_attend_prompt(dev.index, rq, rk, rv, ro, cu_p, cu.shape[0] - 1, n, heads, kv, dim, d,
+                                     dim ** -0.5 if scale is None else scale, err, s)
+        if st:
+            raise MoEError(st, "moe_attend_prompt")
     return out

@@ -9,14 +9,14 @@
 // exponential unit (16 per cycle and SM), so both have to run at the same time.
 //
 // One CTA takes 256 query rows of one head as two tiles of 128, whose softmax and products
-// alternate: while one tile's weights are formed by four warps, the tensor pipe works for
-// the other.  Warp roles, joined by mbarriers:
+// alternate: while one tile's weights are formed, the tensor pipe works for the other.
+// Warp roles, joined by mbarriers:
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns a row; it reads S from tensor
-//                     memory, keeps the row's maximum and sum in registers, writes P (16-bit)
-//                     over S, and rescales O in tensor memory when the maximum has grown
+//                     memory, keeps the row's maximum and sum in registers, writes P (16-bit) to
+//                     tensor memory, and rescales O there when the maximum has grown
 //   warp 8            TMA of Q, then of K and V tiles (128 keys) into a ring
-//   warp 9            tcgen05.mma: S from shared memory, O with P from tensor memory
-// Tensor memory: S0, S1 (128 columns each; P takes the first 64 of its S), O0, O1 (D each).
+//   warp 9            tcgen05.mma of S, both operands from shared memory
+//   warp 10           tcgen05.mma of O, P from tensor memory and V from shared memory
 // The maximum that a row's exponents refer to moves only when it is exceeded by more than
 // 2^8, so most key tiles rescale nothing; P stays below 256, inside either 16-bit type.
 // P is rounded to the input type (half a step per weight); sums, S and O are fp32.
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kPM = 128;      // query rows of a tile
 constexpr int kPN = 128;      // keys of a tile
-constexpr int kPThreads = 320;
+constexpr int kPThreads = 384;  // three warpgroups, the last with the TMA and MMA warps
 
 struct PromptArgs {
   const int32_t* cu;
@@ -49,28 +49,21 @@ __device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(ok)
-      : "r"(kv_smem(b)), "r"(parity)
+      : "r"(kv_smem(b)), "r"(parity), "r"(1000u)  // suspended for at most this many ns
       : "memory");
   return ok != 0;
 }
-// False after about 2 s, or at once when another role gave up.
-__device__ __noinline__ bool bar_spin(uint64_t* b, uint32_t parity, volatile int* abort) {
-  uint64_t t0, t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  while (!bar_try(b, parity)) {
-    if (*abort) return false;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    if (t - t0 > 2000000000ull) {
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
+// False after 2^21 attempts of at most about a microsecond each, or soon after another role
+// gave up.  Inline: a call here would make the softmax warps save their row of products.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-  return bar_try(b, parity) || bar_spin(b, parity, abort);
+  for (int i = 0; i < (1 << 21); ++i) {
+    if (bar_try(b, parity)) return true;
+    if ((i & 1023) == 1023 && *abort) return false;
+  }
+  *abort = 1;
+  return false;
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(kv_smem(b)) : "memory");
@@ -120,12 +113,10 @@ __device__ __forceinline__ void tm_ld32(uint32_t at, uint32_t* r) {
       : O32("=r", r)
       : "r"(at));
 }
-__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::O32("r", r),
-      "r"(at)
-      : "memory");
+__device__ __forceinline__ void tm_ld16(uint32_t at, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : O16("=r", r)
+               : "r"(at));
 }
 __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* r) {
   asm volatile(
@@ -136,10 +127,17 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* r) {
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Uses of loaded registers cannot be scheduled before the wait: they pass through here after it.
+__device__ __forceinline__ void tm_landed16(uint32_t* r) { asm volatile("" : O16("+r", r)); }
 __device__ __forceinline__ void tm_landed32(uint32_t* r) { asm volatile("" : O32("+r", r)); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -160,6 +158,29 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return r;
 }
 
+// Pairs of fp32: one instruction for two.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int D>
 struct PromptSmem {
   static constexpr int kStages = D == 64 ? 4 : 2;
@@ -169,22 +190,35 @@ struct PromptSmem {
   static constexpr uint32_t kBars = kEnd, kBytes = kEnd + 512 + 1024;  // + alignment to 1024
 };
 
+// Tensor memory columns.  P has columns of its own, so that S is free as soon as the softmax warps have it in
+// registers: with D = 64 each query tile has an S, with D = 128 there is room for one, which
+// the two tiles take in turn.
+template <int D>
+struct PromptTmem {
+  static constexpr int kS = D == 64 ? 2 : 1;
+  __device__ static constexpr uint32_t s(int w) { return kS == 2 ? 128 * w : 0; }
+  __device__ static constexpr uint32_t p(int w) { return 128 * kS + 64 * w; }
+  __device__ static constexpr uint32_t o(int w) { return 128 * kS + 128 + D * w; }
+};
+static_assert(PromptTmem<64>::kS * 128 + 128 + 2 * 64 <= 512 && PromptTmem<128>::kS * 128 + 128 + 2 * 128 <= 512, "512 columns");
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPThreads, 1)
     attend_prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv) {
   using S = PromptSmem<D>;
+  using M = PromptTmem<D>;
   constexpr int ST = S::kStages, NB = D / 64;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (kv_smem(raw) & 1023u)) & 1023u);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + S::kBars);
-  uint64_t *s_full = q_full + 2, *p_full = q_full + 4, *o_done = q_full + 6, *fix = q_full + 8;
-  uint64_t *k_full = q_full + 9, *k_empty = k_full + ST, *v_full = k_empty + ST, *v_empty = v_full + ST;
+  uint64_t *s_full = q_full + 2, *p_full = q_full + 4, *o_done = q_full + 6, *p_half = q_full + 8, *s_free = q_full + 10, *fix = q_full + 12;
+  uint64_t *k_full = q_full + 13, *k_empty = k_full + ST, *v_full = k_empty + ST, *v_empty = v_full + ST;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(v_empty + ST);
   int* found = reinterpret_cast<int*>(tmem_at + 1);  // sequence's first row, rows, block
   volatile int* abort = found + 3;
   int* wsum = found + 4;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // Which sequence and block: blocks are numbered along the sequences, the last first (the
   // longest rows of a sequence start first), heads of a block side by side.
@@ -196,6 +230,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       bar_init(q_full + i, 1);
       bar_init(s_full + i, 1);
       bar_init(p_full + i, 4);
+      bar_init(p_half + i, 4);
+      bar_init(s_free + i, 4);
       bar_init(o_done + i, 1);
     }
     bar_init(fix, 1);
@@ -259,12 +295,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int n_kv = n1 ? n1 : n0;
   const uint32_t qa = kv_smem(sm + S::kQ), ka = kv_smem(sm + S::kK), va = kv_smem(sm + S::kV);
 
+  // Registers: the softmax warps hold a row of 128 products each; 2 x 208 + 88 are the
+  // 3 x 168 that the kernel was launched with.
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
     const int w = warp >> 2, row = (warp & 3) * 32 + lane;
     const int nt = w ? n1 : n0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t st = tmem + lanes + w * 128, ot = tmem + lanes + 256 + w * D;
+    const uint32_t st = tmem + lanes + M::s(w), pt = tmem + lanes + M::p(w), ot = tmem + lanes + M::o(w);
     float m = -INFINITY, l = 0.0f;  // m in units of S
     bool ok = true;
     for (int j = 0; j < nt && ok; ++j) {
@@ -278,19 +319,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tm_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) tm_landed32(s + 32 * c);
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(s_free + w);
       if (j == nt - 1) {  // the diagonal tile: keys behind the row (and so behind the sequence)
 #pragma unroll
         for (int c = 0; c < 128; ++c) f[c] = c > row ? -INFINITY : f[c];
       }
       float mx[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
-      for (int c = 4; c < 128; c += 4) {
+      for (int c = 4; c < 124; c += 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], f[c + i]);
+        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], f[c + i], f[c + 4 + i]);
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool grow = (top - m) * a.scale2 > 8.0f || m == -INFINITY;
-      if (__any_sync(0xffffffffu, grow)) {
+      const float top = max3(max3(mx[0], mx[1], f[124]), max3(mx[2], mx[3], f[125]), fmaxf(f[126], f[127]));
+      if (__any_sync(0xffffffffu, (top - m) * a.scale2 > 8.0f)) {
         const float mn = fmaxf(m, top);
         const float al = m == mn ? 1.0f : ex2((m - mn) * a.scale2);
         m = mn;
@@ -300,32 +343,57 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (!ok) break;
           tc_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tm_ld32(ot + c, o);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tm_ld16(ot + c, o);
             tm_wait_ld();
-            tm_landed32(o);
+            tm_landed16(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tm_st32(ot + c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tm_st16(ot + c, o);
           }
         }
       }
+      // A part of the weights by a polynomial on the FMA pipe instead of the exponential unit was
+      // tried (an eighth to a half of them): 1216..1255 against 1255 TFLOP/s, the issue slots being taken as well.
       const float off = -m * a.scale2;
-      float sum[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t p[16];
+      const uint64_t sc = f2(a.scale2, a.scale2), of = f2(off, off);
+      uint64_t sum[4] = {0, 0, 0, 0};
+      auto weights = [&](int c, uint32_t(&p)[16]) {
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float x = ex2(fmaf(f[c + i], a.scale2, off)), y = ex2(fmaf(f[c + i + 1], a.scale2, off));
-          sum[i & 2] += x;
-          sum[(i & 2) + 1] += y;
+          const uint64_t v = fma2(f2(f[c + i], f[c + i + 1]), sc, of);
+          float x, y;
+          unpack(v, x, y);
+          x = ex2(x);
+          y = ex2(y);
+          sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], f2(x, y));
           p[i >> 1] = pack2<T>(x, y);
         }
-        tm_st16(st + c / 2, p);
+      };
+      uint32_t p[16];
+      weights(0, p);
+      if (j > 0) {  // P of the tile before must have been used
+        ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (j - 1) & 1, abort));
+        if (!ok) break;
+        tc_after();
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tm_st16(pt, p);
+      weights(32, p);
+      tm_st16(pt + 16, p);
+      tm_wait_st();  // the first half of P V can start
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(p_half + w);
+      weights(64, p);
+      tm_st16(pt + 32, p);
+      weights(96, p);
+      tm_st16(pt + 48, p);
+      {
+        float x, y;
+        unpack(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+        l += x + y;
+      }
       tm_wait_st();
       tc_before();
       __syncwarp();
@@ -398,57 +466,79 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (lane == 0) bar_arrive(v_full + s);
       }
     }
-  } else if (lane == 0) {
+  } else if (warp < 11) {
     // ---------------------------------------------------------------- MMA
-    constexpr uint32_t ty = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    // A whole warp walks the loop and one elected lane issues: descriptors and barriers then live in
+    // uniform registers, where the instructions take them.  (With a single lane in the branch every
+    // product cost some 65 cycles of register moves and every wait 250.)  S and P V are
+    // independent but for their barriers, so each has a warp: one warp for both spends half a
+    // turn in waits that come one after the other.
+    constexpr uint32_t ty = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t base = (1u << 4) | (ty << 7) | (ty << 10) | ((uint32_t)(kPM >> 4) << 24);
-    constexpr uint32_t id_s = base | ((uint32_t)(kPN >> 3) << 17);
-    constexpr uint32_t id_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
-    auto s_mma = [&](int w, int j) {
-      const uint32_t q = qa + w * S::kTileB, k = ka + (j % ST) * S::kTileB;
+    const bool leader = elect_one();
+    bool ok = true;
+    if (warp == 9) {
+      // S of key tile j, tile 0 then tile 1; the columns are free when the softmax warps have the
+      // tile before that used them in registers: the other query tile's where they share them, else its own.
+      constexpr uint32_t id_s = base | ((uint32_t)(kPN >> 3) << 17);
+      const uint64_t qd = op_desc(qa, 16), kd = op_desc(ka, 16);
+      for (int j = 0; j < n_kv && ok; ++j) {
+        ok = bar_wait(k_full + j % ST, (j / ST) & 1, abort);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * S::kBox + (kk & 3) * 32;
-        mma_ss(tmem + w * 128, op_desc(q + o, 16), op_desc(k + o, 16), id_s, kk > 0);
-      }
-      commit(s_full + w);
-    };
-    auto o_mma = [&](int w, int j) {
-      const uint32_t v = va + (j % ST) * S::kTileB;
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || j >= (w ? n1 : n0)) continue;
+          if (j == 0) ok = bar_wait(q_full + w, 0, abort);
+          if (M::kS == 2 || !n1) {
+            if (j > 0 && ok) ok = bar_wait(s_free + w, (j - 1) & 1, abort);
+          } else if (w == 1) {
+            if (ok) ok = j < n0 ? bar_wait(s_free, j & 1, abort) : bar_wait(s_free + 1, (j - 1) & 1, abort);
+          } else if (j > 0 && ok) {
+            ok = bar_wait(s_free + 1, (j - 1) & 1, abort);
+          }
+          if (!ok) continue;
+          tc_after();
+          if (leader) {
+            const uint64_t q = qd + w * (S::kTileB >> 4), k = kd + (j % ST) * (S::kTileB >> 4);
 #pragma unroll
-      for (int kk = 0; kk < kPN / 16; ++kk)
-        mma_ts(tmem + 256 + w * D, tmem + w * 128 + kk * 8, op_desc(v + kk * 2048, S::kBox), id_o, j > 0 || kk > 0);
-      commit(o_done + w);
-    };
-    bool ok = bar_wait(k_full, 0, abort) && bar_wait(q_full, 0, abort);
-    if (ok) {
-      tc_after();
-      s_mma(0, 0);
-      if (n1) {
-        ok = bar_wait(q_full + 1, 0, abort);
-        if (ok) s_mma(1, 0);
-      }
-      commit(k_empty);
-    }
-    for (int j = 0; j < n_kv && ok; ++j) {
-      ok = bar_wait(v_full + j % ST, (j / ST) & 1, abort);
-      for (int w = 0; w < 2 && ok; ++w) {
-        const int nt = w ? n1 : n0;
-        if (j < nt) {
-          ok = bar_wait(p_full + w, j & 1, abort);
-          if (!ok) break;
-          tc_after();
-          o_mma(w, j);
-        }
-        if (j + 1 < nt) {
-          ok = bar_wait(k_full + (j + 1) % ST, ((j + 1) / ST) & 1, abort);
-          if (!ok) break;
-          tc_after();
-          s_mma(w, j + 1);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4;
+              mma_ss(tmem + M::s(w), q + o, k + o, id_s, kk > 0);
+            }
+            commit(s_full + w);
+            if (w == 1 || !n1) commit(k_empty + j % ST);
+          }
+          __syncwarp();
         }
       }
-      commit(v_empty + j % ST);
-      if (j + 1 < n_kv) commit(k_empty + (j + 1) % ST);
+    } else {
+      constexpr uint32_t id_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
+      const uint64_t vd = op_desc(va, S::kBox);
+      for (int j = 0; j < n_kv && ok; ++j) {
+        ok = bar_wait(v_full + j % ST, (j / ST) & 1, abort);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j >= (w ? n1 : n0)) continue;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (ok) ok = bar_wait((half ? p_full : p_half) + w, j & 1, abort);
+            if (!ok) continue;
+            tc_after();
+            if (leader) {
+              const uint64_t v = vd + (j % ST) * (S::kTileB >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kPN / 32; ++kk) {
+                const int k = half * (kPN / 32) + kk;
+                mma_ts(tmem + M::o(w), tmem + M::p(w) + k * 8, v + k * (2048 >> 4), id_o, j > 0 || k > 0);
+              }
+              if (half) {
+                commit(o_done + w);
+                if (w == 1 || !n1) commit(v_empty + j % ST);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
     }
   }
   tc_before();

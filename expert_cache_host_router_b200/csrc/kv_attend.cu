@@ -15,12 +15,15 @@
 // Products run on mma.sync m16n8k16 with fp32 accumulation: M is 16 keys (then 16
 // channels), N the 8 heads of a group, so 8 query heads cost one instruction.  tcgen05
 // would pad N and M to tiles (128 rows) that a decode step does not have, and both
-// operands would have to be dequantised into shared memory first.  The nibbles become 16-bit floats
-// by bit operations alone: (w & mask) | magic is base + q exactly, and for the keys
-// -(base + 8) sum_c q_c is the accumulator's initial value, so the product of the codes
-// q - 8 comes out without a subtraction; the block scale multiplies the fp32 partial sum.
-// Values are (q - 8) d rounded to fp16 (half a step, 2^-11) and weights p fp16 too, for
-// both input types: cached values are within the fp16 range by construction.
+// operands would have to be dequantised into shared memory first.  What limits the kernel
+// besides the bytes is the integer pipe (2 warp instructions a cycle), so the nibbles become
+// fp16 by few operations: (w & mask) | magic is base + q exactly.  For the keys (base 64) the
+// accumulator starts at -72 sum_c q_c, which takes the base out without a subtraction, and
+// the block scale multiplies the fp32 partial sum.  Values use base 1024 or 64, whichever the
+// nibble's place gives without a shift, and become (q - 8) d rounded to fp16 (half a step,
+// 2^-11); weights p are fp16 too.  Queries are scaled by a power of two per head to the fp16
+// range (exact but for channels 2^-24 below the head's largest); cached values are within
+// that range by construction.
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -119,41 +122,20 @@ __device__ __forceinline__ void kv_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(kv_smem(bar)), "r"(bytes) : "memory");
 }
 
-// A 16-bit type as the matrix products take it: base + q by bit operations.
-template <typename T>
-struct Magic;
-template <>
-struct Magic<__half> {  // 64 + q with q at mantissa bits 4..7
-  static constexpr uint32_t mask = 0x00F000F0u, bits = 0x54005400u;
-  static constexpr float base = 64.0f;
-  static constexpr int at = 4;
-};
-template <>
-struct Magic<__nv_bfloat16> {  // 128 + q with q at mantissa bits 0..3
-  static constexpr uint32_t mask = 0x000F000Fu, bits = 0x43004300u;
-  static constexpr float base = 128.0f;
-  static constexpr int at = 0;
-};
-template <typename T, int N>  // nibble N of both halves of w
-__device__ __forceinline__ uint32_t magic(uint32_t w) {
-  constexpr int sh = 4 * N - Magic<T>::at;
-  const uint32_t s = sh > 0 ? w >> sh : w << -sh;
-  return (s & Magic<T>::mask) | Magic<T>::bits;
+template <uint32_t MASK, uint32_t BITS>
+__device__ __forceinline__ uint32_t masked(uint32_t w) {  // (w & MASK) | BITS in one instruction
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "n"(BITS));
+  return r;
 }
+constexpr uint32_t kAt0 = 0x000F000Fu, k1024 = 0x64006400u;  // nibble at mantissa bits 0..3: 1024 + q
+constexpr uint32_t kAt4 = 0x00F000F0u, k64 = 0x54005400u;    // at bits 4..7: 64 + q
 
-template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1, const float (&c)[4]) {
-  if constexpr (sizeof(T) == 2 && Magic<T>::at == 0)
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-  else
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -201,15 +183,31 @@ struct Line {  // walks the segments of [lin, end)
   }
 };
 
+// The groups of one warp, in order: of every segment its share of consecutive groups.
+struct Walk {
+  Line line;
+  Segment s;
+  int g, end;  // groups [g, end) of the segment are still to come
+  bool more;
+  __device__ __forceinline__ void segment(const int* pre, int items, int n_seqs, int warp) {
+    more = line.next(pre, items, n_seqs, s);
+    const int n = more ? (s.s1 - s.s0 + kGT - 1) / kGT : 0;
+    g = n * warp / kAW;
+    end = n * (warp + 1) / kAW;
+  }
+};
+
 template <int D, int NT>
 struct AttendSmem {
   static constexpr int kStages = NT == 1 ? 2 : 4;
   static constexpr int kTile = 18 * D, kStage = kGT * kTile;
-  static constexpr int kFrag = (D / 4) * NT + 4 * NT;  // floats of a thread's state: o, then m and l of its columns
+  static constexpr int kFrag = (D / 4 + 4) * NT;  // floats of a thread's state: o, then m and l of its columns
   static constexpr int kRing = kAW * kStages * kStage;
-  static constexpr int kMerge = (kAW / 2) * 32 * kFrag * 4;
-  static constexpr int kBars = kRing + kMerge;
-  static constexpr int kTmp = kBars + kAW * kStages * 8;
+  // The four-stage ring leaves no room beside it: that kernel joins its warps in two halves.
+  static constexpr int kMergeWarps = NT == 1 ? kAW : kAW / 2;
+  static constexpr int kBars = kRing + kMergeWarps * 32 * kFrag * 4;
+  static constexpr int kWalk = kBars + kAW * kStages * 8;  // two walks a warp: kept here between uses, not in registers
+  static constexpr int kTmp = kWalk + kAW * 2 * (int)sizeof(Walk);
   static constexpr int kPre = kTmp + 64;
   static int bytes(int n_seqs) { return kPre + (n_seqs + 1) * 4; }
 };
@@ -236,116 +234,134 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
   const int run = attend_run(a, total, gridDim.x);
   const int lin0 = blockIdx.x * run;
   if ((int64_t)blockIdx.x * run >= total) return;
-  Line cons{lin0, min(total, lin0 + run), 0};
-  {  // first sequence of the run
-    int lo = 0, hi = c.n_seqs - 1;
+  Walk* walks = reinterpret_cast<Walk*>(sm + S::kWalk) + 2 * warp;  // [0] what is computed, [1] what is looked up
+  {
+    Walk w{};
+    w.line = Line{lin0, min(total, lin0 + run), 0};
+    int lo = 0, hi = c.n_seqs - 1;  // first sequence of the run
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (pre[mid] * items <= lin0) lo = mid; else hi = mid - 1;
     }
-    cons.b = lo;
+    w.line.b = lo;
+    w.segment(pre, items, c.n_seqs, warp);
+    if (lane < 2) walks[lane] = w;
+    __syncwarp();
   }
 
-  // Producer side (all lanes keep its state, lane 0 issues): groups of this warp in order,
-  // over segment borders.  The page numbers of the group after next are read one step
-  // ahead, so that no copy waits for them.
-  Line prod = cons;
-  Segment ps;
-  bool p_more = prod.next(pre, items, c.n_seqs, ps);
-  int pk = warp;            // group of the segment
-  int pg[kGT], pb[kGT];     // page numbers read ahead, tile within the page
-  Segment as{};             // segment and group of the read-ahead
-  int ak = -1;
-  auto ahead = [&]() {      // next group of this warp: look its pages up
-    while (p_more && ps.s0 + pk * kGT >= ps.s1) {
-      p_more = prod.next(pre, items, c.n_seqs, ps);
-      pk = warp;
-    }
-    ak = p_more ? pk : -1;
-    as = ps;
-    if (ak >= 0) {
-#pragma unroll
-      for (int i = 0; i < kGT; ++i) {
-        const int tile = ps.s0 + pk * kGT + i;
-        const int p = tile / c.tiles_per_page;
-        pb[i] = tile - p * c.tiles_per_page;
-        pg[i] = tile < ps.s1 ? c.table[(int64_t)ps.b * c.table_stride + p] : -2;
+  // Look-ahead: every lane holds the two tiles of one of the next 32 groups of this warp (across segment
+  // borders), looked up by all lanes at once; a lane issues the copies of its group when
+  // its turn comes.
+  int tile_a = -1, tile_b = -1;  // numbers in the pool; -1: no such page, -2: no second tile
+  int turn = 0, held = 0;
+  auto look_up = [&]() {
+    Walk w = walks[1];
+    turn = held = 0;
+    while (held < 32 && w.more) {
+      const int n = min(32 - held, w.end - w.g);
+      const int k = lane - held;
+      if (k >= 0 && k < n) {
+        const int h = w.s.item / a.n_chunks, tile = w.s.s0 + (w.g + k) * kGT;
+        tile_a = kv_tile_number(c, w.s.b, h, tile);
+        tile_b = tile + 1 < w.s.s1 ? kv_tile_number(c, w.s.b, h, tile + 1) : -2;
       }
-      pk += kAW;
+      held += n;
+      w.g += n;
+      if (w.g >= w.end) w.segment(pre, items, c.n_seqs, warp);
     }
+    __syncwarp();
+    if (lane == 0) walks[1] = w;
+    __syncwarp();
   };
-  uint32_t bad = 0;  // stages whose group names a page that is not there
-  auto issue = [&](int stage) {  // copy the group that was looked up, then look up the next
-    if (ak >= 0) {
-      const int h = as.item / a.n_chunks;
-      uint32_t bytes = 0;
-      bad &= ~(1u << stage);
-#pragma unroll
-      for (int i = 0; i < kGT; ++i) {
-        if (pg[i] == -2) continue;
-        if ((unsigned)pg[i] < (unsigned)c.n_pages) bytes += S::kTile; else bad |= 1u << stage;
-      }
-      if (lane == 0) {
-        kv_expect(bars + stage, bytes);
-#pragma unroll
-        for (int i = 0; i < kGT; ++i)
-          if ((unsigned)pg[i] < (unsigned)c.n_pages)
-            kv_bulk(kv_smem(ring + stage * S::kStage + i * S::kTile),
-                    c.pool + (((int64_t)pg[i] * c.heads + h) * c.tiles_per_page + pb[i]) * S::kTile, S::kTile,
-                    bars + stage);
+  auto issue = [&](int stage) {
+    if (turn == held) look_up();
+    if (lane == turn && turn < held) {
+      uint8_t* dst = ring + stage * S::kStage;
+      const uint8_t* src = c.pool + (int64_t)tile_a * S::kTile;
+      if (tile_a >= 0 && tile_b == tile_a + 1) {
+        kv_expect(bars + stage, 2 * S::kTile);
+        kv_bulk(kv_smem(dst), src, 2 * S::kTile, bars + stage);
+      } else {
+        // a missing page's keys get NaN scales, which makes the row's output NaN
+        if (tile_a < 0 || tile_b == -1)
+          for (int i = 0; i < D / 2; ++i) reinterpret_cast<uint16_t*>(dst + 16 * D + (tile_a < 0 ? 0 : S::kTile))[i] = 0x7E00;
+        kv_expect(bars + stage, (tile_a >= 0 ? S::kTile : 0) + (tile_b >= 0 ? S::kTile : 0));
+        if (tile_a >= 0) kv_bulk(kv_smem(dst), src, S::kTile, bars + stage);
+        if (tile_b >= 0) kv_bulk(kv_smem(dst + S::kTile), c.pool + (int64_t)tile_b * S::kTile, S::kTile, bars + stage);
       }
     }
-    ahead();
+    turn = min(turn + 1, held);
   };
-  ahead();
 #pragma unroll
   for (int s = 0; s < ST; ++s) issue(s);
 
   int stage = 0;
   uint32_t phase = 0;
   bool alive = true;
-  Segment sg;
-  while (cons.next(pre, items, c.n_seqs, sg)) {
+  while (walks[0].more) {
+    const Segment sg = walks[0].s;
     const int h = sg.item / a.n_chunks, chunk = sg.item - h * a.n_chunks;
-    const int len = attend_len(c, a, sg.b);
     const int n_heads = min(COLS, a.group - chunk * COLS);  // query heads of this item
     const int h0 = h * a.group + chunk * COLS;
     // Query fragments: column n = g of each 8 heads; within a block the channels of the two
     // 16-deep steps are 4t + {0, 2, 1, 3} and 16 more, the order that the nibbles come in.
     uint32_t qf[NT][NB][4];
-    float qi[NT][NB][2];  // -(base + 8) * sum of a block's channels, for columns 2t and 2t + 1
+    float qi[NT][NB][2];  // -72 times the sum of a block's channels, for columns 2t and 2t + 1
+    float sc[NT][2];      // their scale, with the power of two that the queries were divided by
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const bool has = n * 8 + g < n_heads;
       const T* qp = static_cast<const T*>(a.q) + sg.b * a.q_seq + (int64_t)(h0 + n * 8 + (has ? g : 0)) * a.q_head + 4 * t;
+      uint16_t e[NB][2][4] = {};
+      if (has) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint16_t* at = reinterpret_cast<const uint16_t*>(qp + nb * 32 + hf * 16);
+            if (a.vec) {
+              *reinterpret_cast<uint2*>(e[nb][hf]) = *reinterpret_cast<const uint2*>(at);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[nb][hf][i] = at[i];
+            }
+          }
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NB * 8; ++i) top = fmaxf(top, fabsf(to_float(reinterpret_cast<const T*>(e)[i])));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^-x and 2^x, x the exponent of the largest channel (0 for none, infinity or NaN)
+      int x = (int)(__float_as_uint(top) >> 23) - 127;
+      if (top == 0.0f || x > 127) x = 0;
+      x = max(min(x, 126), -60);  // smaller queries are 0 to any product
+      const float down = __uint_as_float((uint32_t)(127 - x) << 23), up = a.scale2 * exp2f((float)x);
+      sc[n][0] = __shfl_sync(0xffffffffu, up, 8 * t);
+      sc[n][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float sum = 0.0f;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          uint16_t e[4] = {0, 0, 0, 0};
-          if (has) {
-            if (a.vec) {
-              *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(qp + nb * 32 + hf * 16);
-            } else {
+          __half r[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) e[i] = reinterpret_cast<const uint16_t*>(qp + nb * 32 + hf * 16)[i];
-            }
+          for (int i = 0; i < 4; ++i) {
+            r[i] = __float2half_rn(to_float(reinterpret_cast<const T*>(e[nb][hf])[i]) * down);
+            sum += __half2float(r[i]);
           }
-          qf[n][nb][2 * hf] = e[0] | (uint32_t)e[2] << 16;
-          qf[n][nb][2 * hf + 1] = e[1] | (uint32_t)e[3] << 16;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum += to_float(*reinterpret_cast<const T*>(&e[i]));
+          qf[n][nb][2 * hf] = __half_as_ushort(r[0]) | (uint32_t)__half_as_ushort(r[2]) << 16;
+          qf[n][nb][2 * hf + 1] = __half_as_ushort(r[1]) | (uint32_t)__half_as_ushort(r[3]) << 16;
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -(Magic<T>::base + 8.0f);
+        sum *= -72.0f;
         qi[n][nb][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
         qi[n][nb][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       }
     }
     float o[NT][NB][2][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];  // m in units of the unscaled products
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -353,23 +369,26 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.0f;
     }
-    float* zrow = SCORED ? a.z + ((int64_t)(sg.b * items + sg.item) * a.max_len) * COLS : nullptr;
 
-    for (int k = warp; sg.s0 + k * kGT < sg.s1; k += kAW) {
+    int n_groups = walks[0].end - walks[0].g;
+    // keys of the segment from this warp's first group on
+    const int key0 = (sg.s0 + walks[0].g * kGT) * kTileTok;
+    int left = min(attend_len(c, a, sg.b), sg.s1 * kTileTok) - key0;
+    float* zrow = SCORED ? a.z + ((int64_t)(sg.b * items + sg.item) * a.max_len + key0) * COLS + 2 * t : nullptr;
+    for (; n_groups > 0; --n_groups, left -= kGT * kTileTok) {
       if (alive && !kv_mbar_try(bars + stage, phase) && !kv_mbar_spin(bars + stage, phase)) {
         alive = false;
         kv_flag(c.error, MOE_DEVERR_TMA);
       }
       const uint8_t* base = ring + stage * S::kStage;
-      const int tile0 = sg.s0 + k * kGT;
-      const int left = min(len, sg.s1 * kTileTok) - tile0 * kTileTok;  // keys of this group
+      const bool tail = left < kGT * kTileTok;
       float z[NT][kGT][4];
 #pragma unroll
       for (int i = 0; i < kGT; ++i) {
         const uint8_t* tl = base + i * S::kTile;
         // keys: lane (g, t) has word t of every block of rows g and g + 8
         uint32_t kw[2][NB];
-        __half ks[2][NB];
+        __half2 ks[2][NB / 2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if constexpr (NB == 4) {
@@ -381,43 +400,40 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
           }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[n][i][e] = 0.0f;
-#pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          uint32_t a0[4], a1[4];
-          a0[0] = magic<T, 0>(kw[0][nb]), a0[1] = magic<T, 1>(kw[0][nb]), a0[2] = magic<T, 2>(kw[0][nb]), a0[3] = magic<T, 3>(kw[0][nb]);
-          a1[0] = magic<T, 0>(kw[1][nb]), a1[1] = magic<T, 1>(kw[1][nb]), a1[2] = magic<T, 2>(kw[1][nb]), a1[3] = magic<T, 3>(kw[1][nb]);
-          const float d0 = __half2float(ks[0][nb]), d1 = __half2float(ks[1][nb]);
+          const uint32_t w0 = kw[0][nb], w1 = kw[1][nb];
+          const uint32_t a00 = masked<kAt4, k64>(w0 * 16), a01 = masked<kAt4, k64>(w0), a02 = masked<kAt4, k64>(w0 >> 4),
+                         a03 = masked<kAt4, k64>(w0 >> 8);
+          const uint32_t a10 = masked<kAt4, k64>(w1 * 16), a11 = masked<kAt4, k64>(w1), a12 = masked<kAt4, k64>(w1 >> 4),
+                         a13 = masked<kAt4, k64>(w1 >> 8);
+          const float d0 = nb & 1 ? __high2float(ks[0][nb / 2]) : __low2float(ks[0][nb / 2]);
+          const float d1 = nb & 1 ? __high2float(ks[1][nb / 2]) : __low2float(ks[1][nb / 2]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float s[4];
             const float ini[4] = {qi[n][nb][0], qi[n][nb][1], qi[n][nb][0], qi[n][nb][1]};
-            mma16816<T>(s, a0[0], a1[0], a0[2], a1[2], qf[n][nb][0], qf[n][nb][1], ini);
-            mma16816<T>(s, a0[1], a1[1], a0[3], a1[3], qf[n][nb][2], qf[n][nb][3], s);
-            z[n][i][0] = fmaf(s[0], d0, z[n][i][0]);
-            z[n][i][1] = fmaf(s[1], d0, z[n][i][1]);
-            z[n][i][2] = fmaf(s[2], d1, z[n][i][2]);
-            z[n][i][3] = fmaf(s[3], d1, z[n][i][3]);
+            mma16816(s, a00, a10, a02, a12, qf[n][nb][0], qf[n][nb][1], ini);
+            mma16816(s, a01, a11, a03, a13, qf[n][nb][2], qf[n][nb][3], s);
+            z[n][i][0] = nb ? fmaf(s[0], d0, z[n][i][0]) : s[0] * d0;
+            z[n][i][1] = nb ? fmaf(s[1], d0, z[n][i][1]) : s[1] * d0;
+            z[n][i][2] = nb ? fmaf(s[2], d1, z[n][i][2]) : s[2] * d1;
+            z[n][i][3] = nb ? fmaf(s[3], d1, z[n][i][3]) : s[3] * d1;
           }
         }
       }
-      const bool tail = left < kGT * kTileTok, broken = !alive || (bad >> stage & 1);
+      if (tail || !alive) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < kGT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (!alive) z[n][i][e] = __int_as_float(0x7fc00000);
+              if (i * kTileTok + g + 8 * (e >> 1) >= left) z[n][i][e] = -INFINITY;
+            }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kGT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = z[n][i][e] * a.scale2;
-            const int key = i * kTileTok + g + 8 * (e >> 1);
-            if (broken) v = __int_as_float(0x7fc00000);
-            if (tail && key >= left) v = -INFINITY;
-            z[n][i][e] = v;
-            mx[e & 1] = fmaxf(mx[e & 1], v);
-          }
         if (SCORED) {
 #pragma unroll
           for (int i = 0; i < kGT; ++i)
@@ -425,24 +441,29 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
             for (int r = 0; r < 2; ++r) {
               const int key = i * kTileTok + g + 8 * r;
               if (key < left)
-                *reinterpret_cast<float2*>(zrow + (int64_t)(tile0 * kTileTok + key) * COLS + n * 8 + 2 * t) =
-                    make_float2(z[n][i][2 * r], z[n][i][2 * r + 1]);
+                *reinterpret_cast<float2*>(zrow + key * COLS + n * 8) =
+                    make_float2(z[n][i][2 * r] * sc[n][0], z[n][i][2 * r + 1] * sc[n][1]);
             }
         }
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          mx[e] = fmaxf(fmaxf(z[n][0][e], z[n][0][2 + e]), fmaxf(z[n][1][e], z[n][1][2 + e]));
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
           mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
         }
-        // The running maximum moves only when it is exceeded by more than 8 (a factor of 256):
-        // weights stay below 256, far inside fp16, and most groups rescale nothing.
-        const bool move = mx[0] > m[n][0] + 8.0f || mx[1] > m[n][1] + 8.0f || m[n][0] == -INFINITY || m[n][1] == -INFINITY;
+        // The running maximum moves only when it is exceeded by more than 8 in the exponent (a
+        // factor of 256): weights stay below 256, far inside fp16, and most groups rescale
+        // nothing.  m = -inf counts as exceeded unless the products are -inf (or NaN) too.
+        const bool move = (mx[0] - m[n][0]) * sc[n][0] > 8.0f || (mx[1] - m[n][1]) * sc[n][1] > 8.0f;
         if (__any_sync(0xffffffffu, move)) {
           float al[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float mn = fmaxf(m[n][e], mx[e]);
-            al[e] = m[n][e] == mn ? 1.0f : exp2_fast(m[n][e] - mn);
+            al[e] = m[n][e] == mn ? 1.0f : exp2_fast((m[n][e] - mn) * sc[n][e]);
             m[n][e] = mn;
             l[n][e] *= al[e];
           }
@@ -453,11 +474,12 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[n][nb][x][e] *= al[e & 1];
         }
+        const float off0 = -m[n][0] * sc[n][0], off1 = -m[n][1] * sc[n][1];
 #pragma unroll
         for (int i = 0; i < kGT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p = exp2_fast(z[n][i][e] - m[n][e & 1]);
+            const float p = exp2_fast(fmaf(z[n][i][e], sc[n][e & 1], e & 1 ? off1 : off0));
             z[n][i][e] = p;
             l[n][e & 1] += p;
           }
@@ -494,19 +516,19 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const uint32_t off = 0x54805480u;  // 72 = 64 + 8
           uint32_t va[2][4];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            va[r][0] = hmul2(hsub2(magic<__half, 0>(vw[r][nb]), off), vs[r][nb]);
-            va[r][1] = hmul2(hsub2(magic<__half, 1>(vw[r][nb]), off), vs[r][nb]);
-            va[r][2] = hmul2(hsub2(magic<__half, 2>(vw[r][nb]), off), vs[r][nb]);
-            va[r][3] = hmul2(hsub2(magic<__half, 3>(vw[r][nb]), off), vs[r][nb]);
+            const uint32_t w = vw[r][nb], w8 = w >> 8;
+            va[r][0] = hmul2(hsub2(masked<kAt0, k1024>(w), 0x64086408u), vs[r][nb]);   // - 1032
+            va[r][1] = hmul2(hsub2(masked<kAt4, k64>(w), 0x54805480u), vs[r][nb]);     // - 72
+            va[r][2] = hmul2(hsub2(masked<kAt0, k1024>(w8), 0x64086408u), vs[r][nb]);
+            va[r][3] = hmul2(hsub2(masked<kAt4, k64>(w8), 0x54805480u), vs[r][nb]);
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816<__half>(o[n][nb][0], va[0][0], va[0][1], va[1][0], va[1][1], pf[n][0], pf[n][1], o[n][nb][0]);
-            mma16816<__half>(o[n][nb][1], va[0][2], va[0][3], va[1][2], va[1][3], pf[n][0], pf[n][1], o[n][nb][1]);
+            mma16816(o[n][nb][0], va[0][0], va[0][1], va[1][0], va[1][1], pf[n][0], pf[n][1], o[n][nb][0]);
+            mma16816(o[n][nb][1], va[0][2], va[0][3], va[1][2], va[1][3], pf[n][0], pf[n][1], o[n][nb][1]);
           }
         }
       }
@@ -514,155 +536,200 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       issue(stage);
+      if (SCORED) zrow += kGT * kTileTok * COLS;
       if (++stage == ST) {
         stage = 0;
         phase ^= 1;
       }
     }
 
-    // Join the warps, halves at a time: same lane, same fragment.
+    // Join the warps: each leaves its fragments in shared memory, then thread (warp w, lane)
+    // sums fragment entries e4 = w mod 4 of blocks w / 4, w / 4 + 2, .. for its lane.
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
-#pragma unroll
-    for (int half = kAW / 2; half >= 1; half >>= 1) {
-      float* at = merge + (warp & (half - 1)) * 32 * S::kFrag + lane;
-      if (warp >= half && warp < 2 * half) {
+        m[n][e] = m[n][e] * sc[n][e];  // in log2 units from here on
+      }
+    constexpr int MW = S::kMergeWarps;
+    float* mine = merge + (warp % MW) * 32 * S::kFrag + lane;
+    if constexpr (MW < kAW) {  // the upper half first, taken over by the lower one
+      if (warp >= MW) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int i = 0; i < NB * 8; ++i) at[(n * NB * 8 + i) * 32] = (&o[n][0][0][0])[i];
+          for (int i = 0; i < NB * 8; ++i) mine[(n * NB * 8 + i) * 32] = (&o[n][0][0][0])[i];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            at[(NT * NB * 8 + 4 * n + e) * 32] = m[n][e];
-            at[(NT * NB * 8 + 4 * n + 2 + e) * 32] = l[n][e];
+            mine[(NT * NB * 8 + 4 * n + e) * 32] = m[n][e];
+            mine[(NT * NB * 8 + 4 * n + 2 + e) * 32] = l[n][e];
           }
         }
       }
       __syncthreads();
-      if (warp < half) {
+      if (warp < MW) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float x[2], y[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float mo = at[(NT * NB * 8 + 4 * n + e) * 32], lo = at[(NT * NB * 8 + 4 * n + 2 + e) * 32];
+            const float mo = mine[(NT * NB * 8 + 4 * n + e) * 32], lo = mine[(NT * NB * 8 + 4 * n + 2 + e) * 32];
             const float mn = fmaxf(m[n][e], mo);
-            x[e] = m[n][e] == mn || m[n][e] == -INFINITY ? (m[n][e] == mn ? 1.0f : 0.0f) : exp2_fast(m[n][e] - mn);
-            y[e] = mo == mn || mo == -INFINITY ? (mo == mn ? 1.0f : 0.0f) : exp2_fast(mo - mn);
+            x[e] = m[n][e] == mn ? 1.0f : exp2_fast(m[n][e] - mn);
+            y[e] = mo == mn ? 1.0f : exp2_fast(mo - mn);
             m[n][e] = mn;
             l[n][e] = l[n][e] * x[e] + lo * y[e];
           }
 #pragma unroll
           for (int i = 0; i < NB * 8; ++i) {
             float* ov = &o[n][0][0][0];
-            ov[i] = ov[i] * x[i & 1] + at[(n * NB * 8 + i) * 32] * y[i & 1];
+            ov[i] = ov[i] * x[i & 1] + mine[(n * NB * 8 + i) * 32] * y[i & 1];
           }
         }
       }
-      __syncthreads();
     }
-    if (warp == 0) {
-      const bool whole = sg.s0 == 0 && sg.s1 == sg.nt;
-      const int slot = 2 * blockIdx.x + (sg.s0 == 0 ? 1 : 0);
+    if (warp < MW) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < NB * 8; ++i) mine[(n * NB * 8 + i) * 32] = (&o[n][0][0][0])[i];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int col = n * 8 + 2 * t + e;
-          if (whole) {
-            if (SCORED && g == 0) {
-              float* ml = a.ml_whole + ((int64_t)(sg.b * items + sg.item) * COLS + col) * 2;
-              ml[0] = m[n][e];
-              ml[1] = l[n][e];
-            }
-            if (col < n_heads) {
-              const float inv = 1.0f / l[n][e];
-              T* op = static_cast<T*>(a.out) + sg.b * a.o_seq + (int64_t)(h0 + col) * a.o_head + 2 * g;
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                op[nb * 32] = from_float<T>(o[n][nb][0][e] * inv);
-                op[nb * 32 + 1] = from_float<T>(o[n][nb][1][e] * inv);
-                op[nb * 32 + 16] = from_float<T>(o[n][nb][0][2 + e] * inv);
-                op[nb * 32 + 17] = from_float<T>(o[n][nb][1][2 + e] * inv);
-              }
-            }
-          } else {
-            if (g == 0) {
-              float* ml = a.ml + ((int64_t)slot * COLS + col) * 2;
-              ml[0] = m[n][e];
-              ml[1] = l[n][e];
-            }
-            float* pp = a.part + ((int64_t)slot * COLS + col) * D + 2 * g;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              *reinterpret_cast<float2*>(pp + nb * 32) = make_float2(o[n][nb][0][e], o[n][nb][1][e]);
-              *reinterpret_cast<float2*>(pp + nb * 32 + 16) = make_float2(o[n][nb][0][2 + e], o[n][nb][1][2 + e]);
-            }
-          }
+          mine[(NT * NB * 8 + 4 * n + e) * 32] = m[n][e];
+          mine[(NT * NB * 8 + 4 * n + 2 + e) * 32] = l[n][e];
         }
+      }
     }
+    __syncthreads();
+    const bool whole = walks[0].s.s0 == 0 && walks[0].s.s1 == walks[0].s.nt;
+    const int slot = 2 * blockIdx.x + (sg.s0 == 0 ? 1 : 0);
+    const int e4 = warp & 3, e = e4 & 1;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = n * 8 + 2 * t + e;
+      const float* all = merge + lane;
+      float f[MW], M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < MW; ++w) {
+        f[w] = all[w * 32 * S::kFrag + (NT * NB * 8 + 4 * n + e) * 32];
+        M = fmaxf(M, f[w]);
+      }
+#pragma unroll
+      for (int w = 0; w < MW; ++w) {
+        f[w] = f[w] == M ? 1.0f : exp2_fast(f[w] - M);
+        L = fmaf(all[w * 32 * S::kFrag + (NT * NB * 8 + 4 * n + 2 + e) * 32], f[w], L);
+      }
+      if (g == 0 && (warp == 0 || warp == 1)) {  // once for each column
+        if (!whole) reinterpret_cast<float2*>(a.ml)[(int64_t)slot * COLS + col] = make_float2(M, L);
+        else if (SCORED) reinterpret_cast<float2*>(a.ml_whole)[(int64_t)(sg.b * items + sg.item) * COLS + col] = make_float2(M, L);
+      }
+      const float inv = whole ? 1.0f / L : 1.0f;
+#pragma unroll
+      for (int nb = warp >> 2; nb < NB; nb += 2) {
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int w = 0; w < MW; ++w) v[x] = fmaf(all[w * 32 * S::kFrag + (n * NB * 8 + nb * 8 + x * 4 + e4) * 32], f[w], v[x]);
+        const int ch = nb * 32 + 2 * g + 16 * (e4 >> 1);
+        if (!whole) {
+          *reinterpret_cast<float2*>(a.part + ((int64_t)slot * COLS + col) * D + ch) = make_float2(v[0], v[1]);
+        } else if (col < n_heads) {
+          T* op = static_cast<T*>(a.out) + sg.b * a.o_seq + (int64_t)(h0 + col) * a.o_head + ch;
+          op[0] = from_float<T>(v[0] * inv);
+          op[1] = from_float<T>(v[1] * inv);
+        }
+      }
+    }
+    __syncthreads();
+    Walk w = walks[0];
+    w.segment(pre, items, c.n_seqs, warp);
+    __syncwarp();
+    if (lane == 0) walks[0] = w;
+    __syncwarp();
   }
 }
 
 // ------------------------------------------------------------------ second kernel
 
-// CTA x < items joins the partial results of one item (or writes the rows of a sequence
-// without positions: zeros, or NaN when its length cannot be); scored calls then add the
-// weights of keys to the caller's scores, 256 keys of an item's sequence and head a CTA.
-// A position's weight is summed over its heads in order by one thread: no atomics.
+// CTA x < items * 8 NT joins the partial results of one head of an item (or writes the row of
+// a sequence without positions: zeros, or NaN when its length cannot be): the pieces'
+// weights are formed once, one thread each, then every thread sums its channel (the
+// pieces in 256 / D interleaved lines, so that loads are in flight together).  Scored
+// calls then add the weights of keys to the caller's scores, 256 keys of a sequence
+// and KV head a CTA.  A position's weight is summed over its heads in order by one thread: no
+// atomics.
+constexpr int kJoinMax = 1024;  // most pieces of an item: one per CTA of the first kernel
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const AttendArgs a, int n_cta) {
-  constexpr int COLS = 8 * NT;
+  constexpr int COLS = 8 * NT, WAYS = 256 / D;
   __shared__ int tmp[8];
-  __shared__ float sm_m[64 * 16], sm_l[64 * 16];  // per head of a KV head's chunks
+  __shared__ float sm_m[kJoinMax], sm_l[kJoinMax];  // per head of a KV head's chunks; pieces of an item
+  __shared__ float red[256];
   extern __shared__ int pre[];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   attend_prefix(c, a, pre, tmp);
   const int items = c.heads * a.n_chunks;
   const int total = pre[c.n_seqs] * items;
   const int run = attend_run(a, total, n_cta);
   const int all = c.n_seqs * items;
-  if ((int)blockIdx.x < all) {
-    const int b = blockIdx.x / items, item = blockIdx.x % items;
+  // Every CTA waits for the first kernel, also one without work: this grid's end stands for both.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < all * COLS) {
+    const int col = blockIdx.x % COLS, idx = blockIdx.x / COLS;
+    const int b = idx / items, item = idx % items;
     const int h = item / a.n_chunks, chunk = item - h * a.n_chunks;
     const int nt = pre[b + 1] - pre[b];
-    const int n_heads = min(COLS, a.group - chunk * COLS), h0 = h * a.group + chunk * COLS;
-    const int lo = pre[b] * items + item * nt;
-    const int c0 = nt ? lo / run : 0, c1 = nt ? (lo + nt - 1) / run : 0;
-    if (nt && c0 == c1) return;  // one CTA had it whole
-    const float none = attend_len(c, a, b) < 0 ? __int_as_float(0x7fc00000) : 0.0f;
-    if (!nt && none != none && item == 0 && tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
-    for (int x = tid; x < n_heads * D; x += 256) {
-      const int col = x / D, ch = x % D;
-      float v = none;
-      if (nt) {
-        float M = -INFINITY, L = 0.0f, O = 0.0f;
-        bool nan = false;
-        for (int k = c0; k <= c1; ++k) {
-          const int64_t slot = 2 * (int64_t)k + (k == c0 ? 1 : 0);
-          const float mk = a.ml[(slot * COLS + col) * 2], lk = a.ml[(slot * COLS + col) * 2 + 1];
-          const float ok = a.part[(slot * COLS + col) * D + ch];
-          const float mn = fmaxf(M, mk);
-          const float fo = M == mn ? 1.0f : exp2_fast(M - mn), fk = mk == mn ? 1.0f : exp2_fast(mk - mn);
-          nan = nan || lk != lk;
-          L = L * fo + lk * fk;
-          O = O * fo + ok * fk;
-          M = mn;
-        }
-        v = nan ? __int_as_float(0x7fc00000) : O / L;
-      }
-      static_cast<T*>(a.out)[b * a.o_seq + (int64_t)(h0 + col) * a.o_head + ch] = from_float<T>(v);
+    if (col >= a.group - chunk * COLS) return;
+    T* out = static_cast<T*>(a.out) + b * a.o_seq + (int64_t)(h * a.group + chunk * COLS + col) * a.o_head;
+    if (nt == 0) {
+      const bool bad = attend_len(c, a, b) < 0;
+      if (bad && tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
+      if (tid < D) out[tid] = from_float<T>(bad ? __int_as_float(0x7fc00000) : 0.0f);
+      return;
     }
+    const int lo = pre[b] * items + item * nt;
+    const int c0 = lo / run, n = (lo + nt - 1) / run - c0 + 1;
+    if (n == 1) return;  // one CTA had it whole
+    float m = -INFINITY;
+    for (int k = tid; k < n; k += 256) {
+      const float2 ml = reinterpret_cast<const float2*>(a.ml)[(2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * COLS + col];
+      sm_m[k] = ml.x;
+      sm_l[k] = ml.y;
+      m = fmaxf(m, ml.x);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+    const int ch = tid % D, way = tid / D;
+    float L = 0.0f, O = 0.0f;
+#pragma unroll 4
+    for (int k = way; k < n; k += WAYS) {
+      const float f = sm_m[k] == m ? 1.0f : exp2_fast(sm_m[k] - m);
+      L = fmaf(sm_l[k], f, L);
+      O = fmaf(a.part[((2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * COLS + col) * D + ch], f, O);
+    }
+    __syncthreads();
+    red[tid] = O;
+    __syncthreads();
+    float sum = 0.0f;
+    for (int w = 0; w < WAYS; ++w) sum += red[w * D + ch];
+    __syncthreads();
+    red[tid] = L;
+    __syncthreads();
+    float den = 0.0f;
+    for (int w = 0; w < WAYS; ++w) den += red[w * D + ch];
+    if (way == 0) out[ch] = from_float<T>(sum / den);  // a NaN of any piece's sum is in den
     return;
   }
   if (!a.score) return;
   const int per = (a.max_len + 255) / 256;
-  const int x = blockIdx.x - all, bh = x / per, b = bh / c.heads, h = bh % c.heads;
+  const int x = blockIdx.x - all * COLS, bh = x / per, b = bh / c.heads, h = bh % c.heads;
   const int nt = pre[b + 1] - pre[b], len = attend_len(c, a, b);
   const int key0 = (x % per) * 256;
   if (key0 >= len) return;
@@ -727,14 +794,15 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   p->items = (int64_t)c.n_seqs * c.heads * p->chunks;
   const int64_t tiles = p->items * ((max_len + kTileTok - 1) / kTileTok);
   const int per = (max_len + 255) / 256;
-  if (tiles > INT32_MAX / 2 || p->items + (scored ? (int64_t)c.n_seqs * c.heads * per : 0) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (tiles > INT32_MAX / 2 || p->items * 8 * p->nt + (scored ? (int64_t)c.n_seqs * c.heads * per : 0) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const int sms = sm_count(device);
   if (!sms) return MOE_ERR_CUDA;
   // A run is at least one group a warp, so that short caches are spread no thinner than a
   // CTA's warps.
   p->min_run = kAW * kGT;
   const int64_t most = (tiles + p->min_run - 1) / p->min_run;
-  const int fill = (p->nt == 1 ? 2 : 1) * sms;
+  int fill = (p->nt == 1 ? 2 : 1) * sms;
+  if (fill > kJoinMax) fill = kJoinMax;
   p->n_cta = (int)(most < fill ? (most ? most : 1) : fill);
   const int cols = 8 * p->nt;
   size_t off = 0;
@@ -783,7 +851,7 @@ static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendP
                           : launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a, 0);
   if (e != cudaSuccess) return e;
   const int per = (a.max_len + 255) / 256;
-  const int grid = (int)p.items + (a.score ? c.n_seqs * c.heads * per : 0);
+  const int grid = (int)p.items * 8 * NT + (a.score ? c.n_seqs * c.heads * per : 0);
   return launch(kv_attend_join<T, D, NT>, grid, 256, (size_t)(c.n_seqs + 1) * 4, st, true, c, a, p.n_cta);
 }
 

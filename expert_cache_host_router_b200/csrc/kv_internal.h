@@ -61,6 +61,8 @@ inline int kv_check(const moe_kv_pool* c, const moe_kv_table* t, KvView* out) {
   if (t->n_seqs < 0 || t->width < 1 || t->row_stride < t->width) return MOE_ERR_INVALID;
   if (!kv_dim_ok(c->head_dim) || c->page_tokens % kTileTok || c->n_kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)t->width * c->page_tokens > INT32_MAX || t->n_seqs > kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
+  // tiles are numbered in 32 bits: 2^31 of them are 2.4 TB and more
+  if ((int64_t)c->n_pages * (c->page_tokens / kTileTok) > INT32_MAX / c->n_kv_heads) return MOE_ERR_UNSUPPORTED;
   *out = {c->pool_dev, c->n_pages, c->n_kv_heads, c->head_dim, c->page_tokens / kTileTok,
           t->table_dev, t->n_seqs, t->width, t->row_stride, c->error_dev};
   return MOE_OK;
@@ -70,20 +72,21 @@ __device__ __forceinline__ void kv_flag(int32_t* error, int code) {
   if (error) atomicCAS(error, 0, code);
 }
 
-// Tile of position pos (>= 0) of sequence b and head h; null (with the error word set)
+// Number in the pool of tile `tile` of sequence b and head h; -1 (with the error word set)
 // when the table or the page number does not reach it.
-__device__ __forceinline__ uint8_t* kv_tile(const KvView& c, int b, int h, int tile) {
+__device__ __forceinline__ int kv_tile_number(const KvView& c, int b, int h, int tile) {
   const int pg = tile / c.tiles_per_page;
-  if (tile < 0 || pg >= c.width) {
-    kv_flag(c.error, MOE_DEVERR_PAGE);
-    return nullptr;
-  }
-  const int page = c.table[(int64_t)b * c.table_stride + pg];
+  int page = -1;
+  if (tile >= 0 && pg < c.width) page = c.table[(int64_t)b * c.table_stride + pg];
   if ((unsigned)page >= (unsigned)c.n_pages) {
     kv_flag(c.error, MOE_DEVERR_PAGE);
-    return nullptr;
+    return -1;
   }
-  return c.pool + (((int64_t)page * c.heads + h) * c.tiles_per_page + (tile - pg * c.tiles_per_page)) * (18 * c.dim);
+  return (page * c.heads + h) * c.tiles_per_page + (tile - pg * c.tiles_per_page);
+}
+__device__ __forceinline__ uint8_t* kv_tile(const KvView& c, int b, int h, int tile) {
+  const int n = kv_tile_number(c, b, h, tile);
+  return n < 0 ? nullptr : c.pool + (int64_t)n * (18 * c.dim);
 }
 
 __device__ __forceinline__ float to_float(float x) { return x; }
