@@ -494,6 +494,14 @@ def _empty(stream, shape, dtype, dev):
         return _torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _like(stream, t):
+    """The same for a tensor like t (dense, the last dimension contiguous as t's is)."""
+    if stream is None:
+        return _torch.empty_like(t)
+    with _torch.cuda.stream(stream):
+        return _torch.empty_like(t)
+
+
 def kv_pool(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device=0):
     """A zeroed 4-bit key/value cache: uint8 [n_pages, n_kv_heads, page_tokens / 16, 18 * head_dim]
     (page_tokens a multiple of 16, head_dim 64 or 128; layout in include/moe_cache.h)."""
@@ -506,14 +514,16 @@ def kv_pool(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, devi
                        device=torch.device("cuda", device) if isinstance(device, int) else device)
 
 
-def _kv_rows_call(call, name, pool, k, v, table, cu, start, n, stream, error):
-    dev, c = _kv_pool(pool, error, name)
+def _kv_rows_call(call, name, dev, c, k, v, made, table, cu, start, n, stream):
     t = _kv_table(table, dev, name + ": table")
     b, heads, dim, dt = t.n_seqs, c.n_kv_heads, c.head_dim, k.dtype
     cu_p = _ints(cu, 1, dev, name + ": cu", b + 1)
     start_p = None if start is None else _ints(start, 1, dev, name + ": start", b)
-    rk = _rows(k, n, heads, dim, dt, dev, name + ": k")
-    rv = _rows(v, n, heads, dim, dt, dev, name + ": v")
+    if made:  # rows that were made here
+        rk, rv = Rows(k.data_ptr(), heads * dim, dim), Rows(v.data_ptr(), heads * dim, dim)
+    else:
+        rk = _rows(k, n, heads, dim, dt, dev, name + ": k")
+        rv = _rows(v, n, heads, dim, dt, dev, name + ": v")
     d = _dtype(dt, name)
     s = _stream(stream, dev)
     if n and b:
@@ -527,20 +537,22 @@ def kv_store(pool, k, v, table, cu, start=None, error=None, stream=None) -> None
     rows cu[b] .. cu[b + 1] - 1 go to positions start[b] .. (0 .. without start) of sequence
     b, whose pages are table[b].  Rows outside cu[0] .. cu[-1] are padding.  error: int32
     [1], receives MOE_DEVERR_PAGE when a row has no place in the cache (that row is skipped)."""
-    _kv_rows_call(lib().moe_kv_store, "kv_store", pool, k, v, table, cu, start, k.shape[0], stream, error)
+    dev, c = _kv_pool(pool, error, "kv_store")
+    _kv_rows_call(lib().moe_kv_store, "kv_store", dev, c, k, v, False, table, cu, start, k.shape[0], stream)
 
 
 def kv_load(pool, table, cu, start, n_tokens: int, dtype, out=None, error=None, stream=None):
     """Read cached rows back as the values they stand for, addressed as in kv_store.  Returns
     (k, v) [n_tokens, KV heads, head dim]; out: that pair of tensors to write to.  Padding
     rows are left as they were (unspecified in tensors made here)."""
-    if out is None:
-        dev, c = _kv_pool(pool, None, "kv_load")
-        shape = (n_tokens, c.n_kv_heads, c.head_dim)
-        out = _empty(stream, shape, dtype, dev), _empty(stream, shape, dtype, dev)
+    dev, c = _kv_pool(pool, error, "kv_load")
+    made = out is None
+    if made:
+        k = _empty(stream, (n_tokens, c.n_kv_heads, c.head_dim), dtype, dev)
+        out = k, _like(stream, k)
     elif out[0].dtype != dtype:
         _refuse(f"kv_load: out must be {dtype}")
-    _kv_rows_call(lib().moe_kv_load, "kv_load", pool, out[0], out[1], table, cu, start, n_tokens, stream, error)
+    _kv_rows_call(lib().moe_kv_load, "kv_load", dev, c, out[0], out[1], made, table, cu, start, n_tokens, stream)
     return out
 
 
@@ -576,17 +588,21 @@ def kv_attend(pool, q, table, lens, max_len=None, scale=None, score=None, out=No
     d = _dtype(dt, "kv_attend")
     s = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, (n, heads, dim), dt, dev)
+        out = _like(stream, q)
+        ro = Rows(out.data_ptr(), out.stride(0), out.stride(1))
+    else:
+        ro = _rows(out, n, heads, dim, dt, dev, "kv_attend: out")
     if not n:
         return out
     if workspace is None:
-        workspace = _empty(stream, (_attend_workspace(c.n_kv_heads, dim, c.page_tokens, c.device, n, t.width, heads, most,
-                                                      score is not None),), _torch.uint8, dev)
+        size = _attend_workspace(c.n_kv_heads, dim, c.page_tokens, c.device, n, t.width, heads, most, score is not None)
+        workspace = _empty(stream, size, _torch.uint8, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         _refuse(f"kv_attend: workspace must be contiguous on {dev}")
-    ro = _rows(out, n, heads, dim, dt, dev, "kv_attend: out")
+    else:
+        size = workspace.numel() * workspace.element_size()
     st = lib().moe_kv_attend(c, t, lens_p, most, rq, heads, d, dim ** -0.5 if scale is None else scale, ro, sc,
-                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+                             workspace.data_ptr(), size, s)
     if st:
         raise MoEError(st, "moe_kv_attend")
     return out
@@ -614,8 +630,8 @@ def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out
         _refuse(f"kv_evict: keep {keep}")
     s = _stream(stream, dev)
     out_lens = _empty(stream, (n,), _torch.int32, dev)
-    kept = _empty(stream, (n, heads, keep), _torch.int32, dev)
     out_score = _empty(stream, (n, heads, keep), _torch.float32, dev)
+    kept = _empty(stream, (n, heads, keep), _torch.int32, dev)
     if n:
         st = lib().moe_kv_evict(c, t, lens_p, max_len, sc, keep, recent, o, out_lens.data_ptr(), kept.data_ptr(),
                                 out_score.data_ptr(), s)
@@ -647,8 +663,10 @@ def attend_prompt(q, k, v, cu, scale=None, out=None, error=None, stream=None):
     d = _dtype(dt, "attend_prompt")
     s = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, (n, heads, dim), dt, dev)
-    ro = _rows(out, n, heads, dim, dt, dev, "attend_prompt: out")
+        out = _like(stream, q)
+        ro = Rows(out.data_ptr(), out.stride(0), out.stride(1))
+    else:
+        ro = _rows(out, n, heads, dim, dt, dev, "attend_prompt: out")
     if n:
         st = lib().moe_attend_prompt(dev.index, rq, rk, rv, ro, cu_p, cu.shape[0] - 1, n, heads, kv, dim, d,
                                      dim ** -0.5 if scale is None else scale, err, s)

@@ -18,8 +18,8 @@
 // operands would have to be dequantised into shared memory first.  What limits the kernel
 // besides the bytes is the integer pipe (2 warp instructions a cycle), so the nibbles become
 // fp16 by few operations: (w & mask) | magic is base + q exactly.  For the keys (base 64) the
-// accumulator starts at -72 sum_c q_c, which takes the base out without a subtraction, and
-// the block scale multiplies the fp32 partial sum.  Values use base 1024 or 64, whichever the
+// block scale d multiplies the fp32 partial sum, and one more product, of a row's d with
+// -72 sum_c q_c of the blocks (split into three fp16 parts), takes the base out.  Values use base 1024 or 64, whichever the
 // nibble's place gives without a shift, and become (q - 8) d rounded to fp16 (half a step,
 // 2^-11); weights p are fp16 too.  Queries are scaled by a power of two per head to the fp16
 // range (exact but for channels 2^-24 below the head's largest); cached values are within
@@ -51,8 +51,12 @@ struct AttendArgs {
   int64_t s_seq, s_head;
 };
 
-// The line of tiles: sequence b starts at pre[b] * items_per_seq and holds pre[b + 1] - pre[b]
-// tiles for each of its items (KV head and chunk).  Lengths that cannot be are taken as 0.
+// The line: sequence b starts at pre[b] * items_per_seq and every one of its items (KV head
+// and chunk) takes pre[b + 1] - pre[b] places: kItemCost for what an item costs whatever its
+// length (queries, joining the warps), then one for each tile.  A CTA takes the tiles that lie in its
+// run.  Without the cost, runs over short sequences take longest (64 sequences of 129 to
+// 8192: SMs busy 66% of the kernel).  Lengths that cannot be are taken as 0.
+constexpr int kItemCost = 16;
 __device__ __forceinline__ int attend_len(const KvView& c, const AttendArgs& a, int b) {
   const int len = a.lens[b];
   return len < 0 || len > a.max_len || len > c.width * c.tiles_per_page * kTileTok ? -1 : len;
@@ -66,6 +70,7 @@ __device__ __forceinline__ void attend_prefix(const KvView& c, const AttendArgs&
   for (int base = 0; base < c.n_seqs; base += nt) {
     const int b = base + tid;
     int v = b < c.n_seqs ? (max(attend_len(c, a, b), 0) + kTileTok - 1) / kTileTok : 0;
+    if (v) v += kItemCost;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, v, off);
@@ -131,11 +136,18 @@ __device__ __forceinline__ uint32_t masked(uint32_t w) {  // (w & MASK) | BITS i
 constexpr uint32_t kAt0 = 0x000F000Fu, k1024 = 0x64006400u;  // nibble at mantissa bits 0..3: 1024 + q
 constexpr uint32_t kAt4 = 0x00F000F0u, k64 = 0x54005400u;    // at bits 4..7: 64 + q
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+// d += a b and d = a b, 16 x 8 x 16.
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_set(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -170,16 +182,19 @@ struct Segment {
 struct Line {  // walks the segments of [lin, end)
   int lin, end, b;
   __device__ __forceinline__ bool next(const int* pre, int items, int n_seqs, Segment& s) {
-    if (lin >= end) return false;
-    while (pre[b + 1] * items <= lin) ++b;  // lin < end <= pre[n_seqs] * items: ends
-    s.b = b;
-    s.nt = pre[b + 1] - pre[b];
-    const int off = lin - pre[b] * items;
-    s.item = off / s.nt;
-    s.s0 = off - s.item * s.nt;
-    s.s1 = min(s.nt, s.s0 + end - lin);
-    lin += s.s1 - s.s0;
-    return true;
+    while (lin < end) {
+      while (pre[b + 1] * items <= lin) ++b;  // lin < end <= pre[n_seqs] * items: ends
+      const int places = pre[b + 1] - pre[b], off = lin - pre[b] * items;
+      s.b = b;
+      s.nt = places - kItemCost;
+      s.item = off / places;
+      const int at = off - s.item * places, to = min(places, at + end - lin);
+      lin += to - at;
+      s.s0 = max(at - kItemCost, 0);
+      s.s1 = to - kItemCost;
+      if (s.s1 > s.s0) return true;
+    }
+    return false;
   }
 };
 
@@ -306,7 +321,9 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
     // Query fragments: column n = g of each 8 heads; within a block the channels of the two
     // 16-deep steps are 4t + {0, 2, 1, 3} and 16 more, the order that the nibbles come in.
     uint32_t qf[NT][NB][4];
-    float qi[NT][NB][2];  // -72 times the sum of a block's channels, for columns 2t and 2t + 1
+    // -72 times the sum of a block's channels in three parts; a lane's rows of the product are
+    // blocks 2 (t mod 2), + 1 (t < 2: first part and third, else second), as its scales lie.
+    uint32_t qb[NT][2];
     float sc[NT][2];      // their scale, with the power of two that the queries were divided by
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -339,6 +356,7 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
       const float down = __uint_as_float((uint32_t)(127 - x) << 23), up = a.scale2 * exp2f((float)x);
       sc[n][0] = __shfl_sync(0xffffffffu, up, 8 * t);
       sc[n][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
+      float base_sum[NB];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float sum = 0.0f;
@@ -355,10 +373,20 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -72.0f;
-        qi[n][nb][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-        qi[n][nb][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        base_sum[nb] = sum * -72.0f;
       }
+      uint16_t part[2][2];  // this lane's two blocks: [first or second part, third part or nothing]
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float v = NB == 4 && (t & 1) ? base_sum[(2 + i) % NB] : base_sum[i];
+        const __half p1 = __float2half_rn(v), p2 = __float2half_rn(v - __half2float(p1));
+        const __half p3 = __float2half_rn(v - __half2float(p1) - __half2float(p2));
+        const bool twice = NB == 2 && (t & 1);  // two blocks: lanes 0 and 2 alone
+        part[0][i] = twice ? 0 : __half_as_ushort(t < 2 ? p1 : p2);
+        part[1][i] = twice || t >= 2 ? 0 : __half_as_ushort(p3);
+      }
+      qb[n][0] = part[0][0] | (uint32_t)part[0][1] << 16;
+      qb[n][1] = part[1][0] | (uint32_t)part[1][1] << 16;
     }
     float o[NT][NB][2][4];
     float m[NT][2], l[NT][2];  // m in units of the unscaled products
@@ -399,6 +427,16 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
             *reinterpret_cast<uint32_t*>(ks[r]) = *reinterpret_cast<const uint32_t*>(tl + 16 * D + (g + 8 * r) * 4);
           }
         }
+        {
+          uint32_t s2[2];  // scales of the lane's two blocks
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const __half2 lo = ks[r][0], hi = ks[r][NB / 2 - 1];
+            s2[r] = *reinterpret_cast<const uint32_t*>(t & 1 ? &hi : &lo);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_set(z[n][i], s2[0], s2[1], s2[0], s2[1], qb[n][0], qb[n][1]);
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const uint32_t w0 = kw[0][nb], w1 = kw[1][nb];
@@ -411,13 +449,12 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float s[4];
-            const float ini[4] = {qi[n][nb][0], qi[n][nb][1], qi[n][nb][0], qi[n][nb][1]};
-            mma16816(s, a00, a10, a02, a12, qf[n][nb][0], qf[n][nb][1], ini);
-            mma16816(s, a01, a11, a03, a13, qf[n][nb][2], qf[n][nb][3], s);
-            z[n][i][0] = nb ? fmaf(s[0], d0, z[n][i][0]) : s[0] * d0;
-            z[n][i][1] = nb ? fmaf(s[1], d0, z[n][i][1]) : s[1] * d0;
-            z[n][i][2] = nb ? fmaf(s[2], d1, z[n][i][2]) : s[2] * d1;
-            z[n][i][3] = nb ? fmaf(s[3], d1, z[n][i][3]) : s[3] * d1;
+            mma_set(s, a00, a10, a02, a12, qf[n][nb][0], qf[n][nb][1]);
+            mma_add(s, a01, a11, a03, a13, qf[n][nb][2], qf[n][nb][3]);
+            z[n][i][0] = fmaf(s[0], d0, z[n][i][0]);
+            z[n][i][1] = fmaf(s[1], d0, z[n][i][1]);
+            z[n][i][2] = fmaf(s[2], d1, z[n][i][2]);
+            z[n][i][3] = fmaf(s[3], d1, z[n][i][3]);
           }
         }
       }
@@ -449,16 +486,17 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           mx[e] = fmaxf(fmaxf(z[n][0][e], z[n][0][2 + e]), fmaxf(z[n][1][e], z[n][1][2 + e]));
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
-          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
-        }
         // The running maximum moves only when it is exceeded by more than 8 in the exponent (a
         // factor of 256): weights stay below 256, far inside fp16, and most groups rescale
-        // nothing.  m = -inf counts as exceeded unless the products are -inf (or NaN) too.
+        // nothing, nor do they look for the group's maximum beyond each lane's own products.
+        // m = -inf counts as exceeded unless the products are -inf (or NaN) too.
         const bool move = (mx[0] - m[n][0]) * sc[n][0] > 8.0f || (mx[1] - m[n][1]) * sc[n][1] > 8.0f;
         if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+          }
           float al[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -527,8 +565,8 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816(o[n][nb][0], va[0][0], va[0][1], va[1][0], va[1][1], pf[n][0], pf[n][1], o[n][nb][0]);
-            mma16816(o[n][nb][1], va[0][2], va[0][3], va[1][2], va[1][3], pf[n][0], pf[n][1], o[n][nb][1]);
+            mma_add(o[n][nb][0], va[0][0], va[0][1], va[1][0], va[1][1], pf[n][0], pf[n][1]);
+            mma_add(o[n][nb][1], va[0][2], va[0][3], va[1][2], va[1][3], pf[n][0], pf[n][1]);
           }
         }
       }
@@ -681,17 +719,17 @@ __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const Atte
     const int col = blockIdx.x % COLS, idx = blockIdx.x / COLS;
     const int b = idx / items, item = idx % items;
     const int h = item / a.n_chunks, chunk = item - h * a.n_chunks;
-    const int nt = pre[b + 1] - pre[b];
+    const int places = pre[b + 1] - pre[b];
     if (col >= a.group - chunk * COLS) return;
     T* out = static_cast<T*>(a.out) + b * a.o_seq + (int64_t)(h * a.group + chunk * COLS + col) * a.o_head;
-    if (nt == 0) {
+    if (places == 0) {
       const bool bad = attend_len(c, a, b) < 0;
       if (bad && tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
       if (tid < D) out[tid] = from_float<T>(bad ? __int_as_float(0x7fc00000) : 0.0f);
       return;
     }
-    const int lo = pre[b] * items + item * nt;
-    const int c0 = lo / run, n = (lo + nt - 1) / run - c0 + 1;
+    const int lo = pre[b] * items + item * places;
+    const int c0 = (lo + kItemCost) / run, n = (lo + places - 1) / run - c0 + 1;
     if (n == 1) return;  // one CTA had it whole
     float m = -INFINITY;
     for (int k = tid; k < n; k += 256) {
@@ -730,13 +768,13 @@ __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const Atte
   if (!a.score) return;
   const int per = (a.max_len + 255) / 256;
   const int x = blockIdx.x - all * COLS, bh = x / per, b = bh / c.heads, h = bh % c.heads;
-  const int nt = pre[b + 1] - pre[b], len = attend_len(c, a, b);
+  const int places = pre[b + 1] - pre[b], len = attend_len(c, a, b);
   const int key0 = (x % per) * 256;
   if (key0 >= len) return;
   for (int col = tid; col < a.n_chunks * COLS; col += 256) {
     const int chunk = col / COLS, cc = col % COLS, item = h * a.n_chunks + chunk;
-    const int lo = pre[b] * items + item * nt;
-    const int c0 = lo / run, c1 = (lo + nt - 1) / run;
+    const int lo = pre[b] * items + item * places;
+    const int c0 = (lo + kItemCost) / run, c1 = (lo + places - 1) / run;
     float M = -INFINITY, L = 0.0f;
     if (c0 == c1) {
       const float* ml = a.ml_whole + ((int64_t)(b * items + item) * COLS + cc) * 2;
@@ -792,7 +830,7 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   p->nt = group <= 8 ? 1 : 2;
   p->chunks = (group + 8 * p->nt - 1) / (8 * p->nt);
   p->items = (int64_t)c.n_seqs * c.heads * p->chunks;
-  const int64_t tiles = p->items * ((max_len + kTileTok - 1) / kTileTok);
+  const int64_t tiles = p->items * ((max_len + kTileTok - 1) / kTileTok + kItemCost);
   const int per = (max_len + 255) / 256;
   if (tiles > INT32_MAX / 2 || p->items * 8 * p->nt + (scored ? (int64_t)c.n_seqs * c.heads * per : 0) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const int sms = sm_count(device);
