@@ -1,5 +1,7 @@
 // kv_cache.cu -- the 4-bit key/value cache of libmoe: writing rows into it, reading them
 // back, and cutting sequences down to a budget by their accumulated attention weight.
+#include <type_traits>
+
 #include "kv_internal.h"
 
 namespace moe {
@@ -38,23 +40,32 @@ struct Entries {
   int n;
 };
 
-__device__ __forceinline__ bool kv_place(const KvView& c, const RowArgs& a, int tok, int* seq, int64_t* pos) {
-  if (tok < a.cu[0] || tok >= a.cu[c.n_seqs]) return false;  // padding on either side is not a token
-  *seq = kv_find_seq(a.cu, c.n_seqs, tok);
-  *pos = (int64_t)(a.start ? a.start[*seq] : 0) + tok - a.cu[*seq];
-  return true;
-}
-
 // Tokens [tok0, tok0 + n_tok) of this CTA.  A token in an odd row belongs to the one before it, if that is in the
 // same sequence: perhaps the last of the CTA before.
+constexpr int kKnownSeqs = 255;  // bounds of so many sequences are read at once, into shared memory
 __device__ __forceinline__ void kv_entries(const KvView& c, const RowArgs& a, int tok0, int n_tok, Entries* out) {
+  __shared__ int bounds[kKnownSeqs + 1], first_pos[kKnownSeqs + 1];
+  const bool known = c.n_seqs <= kKnownSeqs;
+  if (known) {
+    if ((int)threadIdx.x <= c.n_seqs) {
+      bounds[threadIdx.x] = a.cu[threadIdx.x];
+      first_pos[threadIdx.x] = a.start && (int)threadIdx.x < c.n_seqs ? a.start[threadIdx.x] : 0;
+    }
+    __syncthreads();
+  }
+  const int32_t* cu = known ? bounds : a.cu;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, tok = tok0 + lane;
-    int seq = 0;
+    bool lead = lane < n_tok && tok < a.n_tokens && tok >= cu[0] && tok < cu[c.n_seqs];  // padding on either side is not a token
+    int seq = 0, first = 0, end = 0;
     int64_t pos = 0;
-    bool lead = lane < n_tok && tok < a.n_tokens && kv_place(c, a, tok, &seq, &pos);
-    const int first = lead ? a.cu[seq] : 0, end = lead ? min(a.cu[seq + 1], a.n_tokens) : 0;
-    if (lead && (pos & 1) && tok > first && tok > 0) lead = false;
+    if (lead) {
+      seq = kv_find_seq(cu, c.n_seqs, tok);
+      first = cu[seq];
+      end = min(cu[seq + 1], a.n_tokens);
+      pos = (int64_t)(known ? first_pos[seq] : a.start ? a.start[seq] : 0) + tok - first;
+      if ((pos & 1) && tok > first && tok > 0) lead = false;
+    }
     const uint32_t mask = __ballot_sync(0xffffffffu, lead);
     if (lead) {
       Entry e{-1, tok, (int)(pos & (kTileTok - 1)), !(pos & 1) && tok + 1 < end};
@@ -72,23 +83,27 @@ __device__ __forceinline__ void kv_entries(const KvView& c, const RowArgs& a, in
   __syncthreads();
 }
 
+// 8 channels as they lie in memory, and their values.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+__device__ __forceinline__ void load8(const T* p, Raw8<T>& r) {
   if constexpr (VEC) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
-      const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = to_float(e[i]);
-    } else {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
   } else {
+    T* e = reinterpret_cast<T*>(&r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_float(p[i]);
+    for (int i = 0; i < 8; ++i) e[i] = p[i];
   }
+}
+template <typename T>
+__device__ __forceinline__ void values8(const Raw8<T>& r, float (&x)[8]) {
+  const T* e = reinterpret_cast<const T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = to_float(e[i]);
 }
 
 template <typename T, bool VEC>
@@ -123,11 +138,11 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 // and sum are off by less than 2^-20, so adding 2^-18 puts exact borders on their upper side
 // and moves nothing else across: the codes are the definition's, bit for bit.  A division
 // each made the kernel bound by arithmetic (31 us against 16 us for 16383 tokens of 8 heads of 64).
-template <bool EXACT16>
-__device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t* lo_out, uint32_t* hi_out) {
+template <typename T>
+__device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t lanes, uint32_t* lo_out, uint32_t* hi_out) {
   uint32_t lo = 0, hi = 0;
   float d;
-  if constexpr (EXACT16) {
+  if constexpr (sizeof(T) == 2) {
     uint32_t key = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -135,8 +150,8 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t*
       key = max(key, (u & 0x7FFFFFFFu) | (u >> 31) | (uint32_t)((7 - i) << 1));
     }
     key |= (uint32_t)(3 - j) << 4;
-    key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
-    key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
+    key = max(key, __shfl_xor_sync(lanes, key, 1));
+    key = max(key, __shfl_xor_sync(lanes, key, 2));
     const float m = __uint_as_float((key & 0x7FFFE000u) | key << 31);
     const bool nan = (key & 0x7FFFE000u) > 0x7F800000u;
     d = nan ? __int_as_float(0x7fc00000) : fminf(fmaxf(m * -0.125f, -8188.0f), 8188.0f);
@@ -144,7 +159,8 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t*
     uint32_t q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // round(x / d + 8 + 2^-18) in the low bits of 2^23 + q
-      const float r = fminf(fmaxf(fmaf(x[i], inv, 8.0f + 3.814697265625e-6f), 0.0f), 15.0f);
+      float r = fminf(fmaf(x[i], inv, 8.0f + 3.814697265625e-6f), 15.0f);
+      if (!std::is_same<T, __half>::value) r = fmaxf(r, 0.0f);  // only a limited d gives less: |x| > 65504
       q[i] = __float_as_uint(r + 8388608.0f);
     }
     lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
@@ -159,8 +175,8 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t*
     }
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
-      const float o = __shfl_xor_sync(0xffffffffu, m, off);
-      nan |= __shfl_xor_sync(0xffffffffu, nan, off);
+      const float o = __shfl_xor_sync(lanes, m, off);
+      nan |= __shfl_xor_sync(lanes, nan, off);
       const bool lower = (j & off) != 0;  // the other lane's channels come first
       if (fabsf(o) > fabsf(m) || (lower && fabsf(o) == fabsf(m))) m = o;
     }
@@ -177,43 +193,74 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t*
   return d;
 }
 
-// Rows of a token and head: D / 4 lanes, 8 channels each, the keys' lanes first; a CTA's
-// 256 threads hold 1024 / D rows at a time and walk over its entries, then the heads.
+// How a CTA's threads share its entries and heads: a group of D / 8 lanes takes a row of keys
+// (even warps) or values (odd warps), 8 channels a lane; groups go round the entries, and
+// round the heads where there are fewer entries than groups.
+template <int D>
+struct Share {
+  static constexpr int kLanes = D / 8, kGroups = 4 * 32 / kLanes;
+  int j, block, entry, head, head_step;
+  bool value;
+  uint32_t lanes;  // of the group
+  __device__ __forceinline__ explicit Share(int n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = lane % kLanes;
+    const int group = (warp >> 1) * (32 / kLanes) + lane / kLanes;
+    value = warp & 1;
+    j = in & 3;
+    block = in >> 2;
+    lanes = (uint32_t)((1ull << kLanes) - 1) << (lane - in);
+    head_step = n < kGroups ? kGroups / n : 1;
+    entry = n < kGroups ? group % n : group;
+    head = n < kGroups ? group / n : 0;
+    if (head >= head_step) entry = n;  // a group too many
+  }
+};
+
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(256) kv_store_kernel(const KvView c, const RowArgs a, int n_tok) {
-  constexpr int NB = D / 32, LANES = D / 4, UNITS = 256 / LANES;
+__global__ void __launch_bounds__(256, 4) kv_store_kernel(const KvView c, const RowArgs a, int n_tok) {
+  constexpr int NB = D / 32;
   __shared__ Entries es;
   kv_entries(c, a, blockIdx.x * n_tok, n_tok, &es);
-  const int in = threadIdx.x % LANES, j = in & 3, block = (in % (LANES / 2)) >> 2;
-  const bool value = in >= LANES / 2;
-  const T* src = static_cast<const T*>(value ? a.v : a.k) + block * 32 + j * 8;
-  const int64_t st_tok = value ? a.v_tok : a.k_tok, st_head = value ? a.v_head : a.k_head;
   const int n = es.n;
   if (n == 0) return;
-  int e = threadIdx.x / LANES, h = 0;
-  while (e >= n) e -= n, ++h;
-  while (__any_sync(0xffffffffu, h < c.heads)) {  // the lanes of a warp may be at different heads: all take part in the shuffles
-    const bool live = h < c.heads;
+  const Share<D> sh(n);
+  const int j = sh.j, block = sh.block, t = 2 * (j & 1) + (j >> 1);
+  const T* src = static_cast<const T*>(sh.value ? a.v : a.k) + block * 32 + j * 8;
+  const int64_t st_tok = sh.value ? a.v_tok : a.k_tok, st_head = sh.value ? a.v_head : a.k_head;
+  for (int e = sh.entry; e < n; e += Share<D>::kGroups) {
     const Entry en = es.e[e];
-    const bool put = live && en.at >= 0;
-    float x[2][8] = {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0}};
-    const T* p = src + en.tok * st_tok + h * st_head;
-    if (put) load8<T, VEC>(p, x[0]);
-    if (put && en.both) load8<T, VEC>(p + st_tok, x[1]);
-    uint32_t word[2];
-    __half d[2];
-    const int t = 2 * (j & 1) + (j >> 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t lo, hi;
-      d[i] = __float2half_rn(quantise8<sizeof(T) == 2>(x[i], j, &lo, &hi));
-      // lanes j and j + 2 hold channels 8j.. and 16 + 8j..: together two words of the block
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, j < 2 ? hi : lo, 2);
-      word[i] = j < 2 ? (lo | got << 4) : (got | hi << 4);
+    if (en.at < 0) continue;
+    const T* p = src + en.tok * st_tok + sh.head * st_head;
+    const int64_t head_bytes = (int64_t)c.tiles_per_page * (18 * D);
+    uint8_t* tile = c.pool + en.at + sh.head * head_bytes;
+    const int64_t step = sh.head_step * st_head;
+    // the next head's channels are read before this one's are worked on
+    Raw8<T> next[2];
+    if (sh.head < c.heads) {
+      load8<T, VEC>(p, next[0]);
+      if (en.both) load8<T, VEC>(p + st_tok, next[1]);
     }
-    if (put) {
-      uint8_t* tile = c.pool + en.at + (int64_t)h * c.tiles_per_page * (18 * D);
-      if (!value) {
+    for (int h = sh.head; h < c.heads; h += sh.head_step, tile += sh.head_step * head_bytes) {
+      float x[2][8];
+      values8(next[0], x[0]);
+      values8(next[1], x[1]);
+      p += step;
+      if (h + sh.head_step < c.heads) {
+        load8<T, VEC>(p, next[0]);
+        if (en.both) load8<T, VEC>(p + st_tok, next[1]);
+      }
+      uint32_t word[2];
+      __half d[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i == 1 && !en.both) break;
+        uint32_t lo, hi;
+        d[i] = __float2half_rn(quantise8<T>(x[i], j, sh.lanes, &lo, &hi));
+        // lanes j and j + 2 hold channels 8j.. and 16 + 8j..: together two words of the block
+        const uint32_t got = __shfl_xor_sync(sh.lanes, j < 2 ? hi : lo, 2);
+        word[i] = j < 2 ? (lo | got << 4) : (got | hi << 4);
+      }
+      if (!sh.value) {
         uint8_t* at = tile + en.row * 16 * NB + t * 4 * NB + block * 4;
         __half* sc = reinterpret_cast<__half*>(tile + 16 * D) + en.row * NB + block;
         *reinterpret_cast<uint32_t*>(at) = word[0];
@@ -237,71 +284,104 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const KvView c, const Row
         }
       }
     }
-    e += UNITS;
-    while (e >= n) e -= n, ++h;
   }
 }
 
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(256) kv_load_kernel(const KvView c, const RowArgs a, int n_tok) {
-  constexpr int NB = D / 32, LANES = D / 4, UNITS = 256 / LANES;
+__global__ void __launch_bounds__(256, 6) kv_load_kernel(const KvView c, const RowArgs a, int n_tok) {
+  constexpr int NB = D / 32;
   __shared__ Entries es;
   kv_entries(c, a, blockIdx.x * n_tok, n_tok, &es);
-  const int in = threadIdx.x % LANES, j = in & 3, block = (in % (LANES / 2)) >> 2;
-  const bool value = in >= LANES / 2;
-  T* dst = static_cast<T*>(value ? a.v : a.k) + block * 32 + j * 8;
-  const int64_t st_tok = value ? a.v_tok : a.k_tok, st_head = value ? a.v_head : a.k_head;
-  const int n = es.n, t = 2 * (j & 1), sh = (j >> 1) * 4;
+  const int n = es.n;
   if (n == 0) return;
-  int e = threadIdx.x / LANES, h = 0;
-  while (e >= n) e -= n, ++h;
-  for (; h < c.heads;) {
-    const Entry en = es.e[e];
-    uint32_t w[2][2] = {{0, 0}, {0, 0}};
-    __half d[2] = {__ushort_as_half(0x7e00), __ushort_as_half(0x7e00)};  // NaN where the table does not reach
-    if (en.at >= 0) {
-      const uint8_t* tile = c.pool + en.at + (int64_t)h * c.tiles_per_page * (18 * D);
-      if (!value) {
-        const uint8_t* at = tile + en.row * 16 * NB + t * 4 * NB + block * 4;
-        const __half* sc = reinterpret_cast<const __half*>(tile + 16 * D) + en.row * NB + block;
-        w[0][0] = *reinterpret_cast<const uint32_t*>(at);
-        w[0][1] = *reinterpret_cast<const uint32_t*>(at + 4 * NB);
-        d[0] = sc[0];
-        if (en.both) {
-          w[1][0] = *reinterpret_cast<const uint32_t*>(at + 16 * NB);
-          w[1][1] = *reinterpret_cast<const uint32_t*>(at + 20 * NB);
-          d[1] = sc[NB];
-        }
-      } else {
-        const int pair = en.row >> 1;
-        const uint8_t* at = tile + 8 * D + pair * 32 * NB + 2 * t * 4 * NB + block * 4;
-        uint32_t p[4];
+  const Share<D> share(n);
+  const int j = share.j, block = share.block, t = 2 * (j & 1), sh = (j >> 1) * 4;
+  T* dst = static_cast<T*>(share.value ? a.v : a.k) + block * 32 + j * 8;
+  const int64_t st_tok = share.value ? a.v_tok : a.k_tok, st_head = share.value ? a.v_head : a.k_head;
+  for (int e = share.entry; e < n; e += Share<D>::kGroups) {
+   const Entry en = es.e[e];
+   T* p = dst + en.tok * st_tok + share.head * st_head;
+   const int64_t head_bytes = (int64_t)c.tiles_per_page * (18 * D);
+   const uint8_t* tile = c.pool + en.at + share.head * head_bytes;
+   // words and scales of one head; read for the next head before this one's are worked on
+   auto fetch = [&](uint32_t(&v)[4], __half(&s2)[2]) {
+     if (!share.value) {
+       const uint8_t* at = tile + en.row * 16 * NB + t * 4 * NB + block * 4;
+       const __half* sc = reinterpret_cast<const __half*>(tile + 16 * D) + en.row * NB + block;
+       v[0] = *reinterpret_cast<const uint32_t*>(at);
+       v[1] = *reinterpret_cast<const uint32_t*>(at + 4 * NB);
+       s2[0] = sc[0];
+       if (en.both) {
+         v[2] = *reinterpret_cast<const uint32_t*>(at + 16 * NB);
+         v[3] = *reinterpret_cast<const uint32_t*>(at + 20 * NB);
+         s2[1] = sc[NB];
+       }
+     } else {
+       const int pair = en.row >> 1;
+       const uint8_t* at = tile + 8 * D + pair * 32 * NB + 2 * t * 4 * NB + block * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const uint32_t*>(at + i * 4 * NB);
-        const __half2 s2 = reinterpret_cast<const __half2*>(tile + 17 * D)[pair * NB + block];
-        const bool odd = en.row & 1;
-        const uint32_t s0 = odd ? 0x7632 : 0x5410;
-        w[0][0] = __byte_perm(p[0], p[1], s0), w[0][1] = __byte_perm(p[2], p[3], s0);
-        w[1][0] = __byte_perm(p[0], p[1], 0x7632), w[1][1] = __byte_perm(p[2], p[3], 0x7632);
-        d[0] = odd ? __high2half(s2) : __low2half(s2);
-        d[1] = __high2half(s2);
-      }
+       for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(at + i * 4 * NB);
+       *reinterpret_cast<__half2*>(s2) = reinterpret_cast<const __half2*>(tile + 17 * D)[pair * NB + block];
+     }
+   };
+   const bool have = en.at >= 0;
+   uint32_t v[4] = {0, 0, 0, 0};
+   __align__(4) __half s2[2] = {__ushort_as_half(0x7e00), __ushort_as_half(0x7e00)};  // NaN where the table does not reach
+   if (have && share.head < c.heads) fetch(v, s2);
+   for (int h = share.head; h < c.heads; h += share.head_step, p += share.head_step * st_head) {
+    uint32_t w[2][2];
+    __half d[2];
+    if (!share.value) {
+      w[0][0] = v[0], w[0][1] = v[1], w[1][0] = v[2], w[1][1] = v[3];
+      d[0] = s2[0], d[1] = s2[1];
+    } else {
+      const bool odd = en.row & 1;
+      const uint32_t s0 = odd ? 0x7632 : 0x5410;
+      w[0][0] = __byte_perm(v[0], v[1], s0), w[0][1] = __byte_perm(v[2], v[3], s0);
+      w[1][0] = __byte_perm(v[0], v[1], 0x7632), w[1][1] = __byte_perm(v[2], v[3], 0x7632);
+      d[0] = odd ? s2[1] : s2[0];
+      d[1] = s2[1];
     }
-    T* p = dst + en.tok * st_tok + h * st_head;
+    tile += share.head_step * head_bytes;
+    if (have && h + share.head_step < c.heads) fetch(v, s2);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i == 1 && !en.both) break;
-      const float df = __half2float(d[i]);
+      // codes of channels 2k, 2k + 1 as 1024 + q in fp16, by bit operations (the integer
+      // converter is a quarter as fast); q - 8 and, for fp16, its product with d are exact to one rounding
+      uint32_t c2[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t b2 = __byte_perm(w[i][k >> 1] >> sh, 0, k & 1 ? 0x4342 : 0x4140);
+        c2[k] = (b2 & 0x000F000Fu) | 0x64006400u;
+      }
+      uint32_t r[4];
       float x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // 2^23 + q by bit operations: the converter is a quarter as fast
-        const uint32_t q = w[i][k >> 2] >> (8 * (k & 3) + sh) & 15;
-        x[k] = (__uint_as_float(0x4B000000u | q) - 8388616.0f) * df;
+      for (int k = 0; k < 4; ++k) {
+        const __half2 q = __hsub2(*reinterpret_cast<__half2*>(&c2[k]), __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 v = __hmul2(q, __half2(d[i], d[i]));
+          r[k] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          const float df = __half2float(d[i]);
+          const float2 v = __half22float2(q);
+          x[2 * k] = v.x * df;
+          x[2 * k + 1] = v.y * df;
+        }
       }
-      store8<T, VEC>(p + i * st_tok, x);
+      if constexpr (std::is_same<T, __half>::value) {
+        if (VEC) {
+          *reinterpret_cast<uint4*>(p + i * st_tok) = make_uint4(r[0], r[1], r[2], r[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(p + i * st_tok)[k] = (uint16_t)(r[k >> 1] >> (16 * (k & 1)));
+        }
+      } else {
+        store8<T, VEC>(p + i * st_tok, x);
+      }
     }
-    e += UNITS;
-    while (e >= n) e -= n, ++h;
+   }
   }
 }
 
