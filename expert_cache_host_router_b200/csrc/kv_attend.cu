@@ -24,8 +24,6 @@
 // 2^-11); weights p are fp16 too.  Queries are scaled by a power of two per head to the fp16
 // range (exact but for channels 2^-24 below the head's largest); cached values are within
 // that range by construction.
-#include <type_traits>
-
 #include "kv_internal.h"
 
 namespace moe {
@@ -42,10 +40,12 @@ struct AttendArgs {
   int max_len, group, n_chunks;  // query heads per KV head; chunks of 8 NT heads that they are split into
   float scale2;                  // scale * log2(e)
   int min_run;                   // tiles a CTA takes at least
+  int join_cols;                 // heads of a joining CTA: 1, or 8 NT
   int vec;                       // rows of q can be read 8 bytes at a time
   float* part;                   // [2 CTAs][8 NT][D] partial outputs, unnormalised
   float* ml;                     // [2 CTAs][8 NT][2] their (m, l)
   float* ml_whole;               // [items][8 NT][2] (m, l) of the items that one CTA has whole (scored calls)
+  int2* pieces;                  // [items] first CTA and number of CTAs of the items that have positions
   float* z;                      // [items][max_len][8 NT] scaled products in log2 units (scored calls)
   float* score;                  // or null
   int64_t s_seq, s_head;
@@ -53,10 +53,11 @@ struct AttendArgs {
 
 // The line: sequence b starts at pre[b] * items_per_seq and every one of its items (KV head
 // and chunk) takes pre[b + 1] - pre[b] places: kItemCost for what an item costs whatever its
-// length (queries, joining the warps), then one for each tile.  A CTA takes the tiles that lie in its
-// run.  Without the cost, runs over short sequences take longest (64 sequences of 129 to
-// 8192: SMs busy 66% of the kernel).  Lengths that cannot be are taken as 0.
-constexpr int kItemCost = 16;
+// length (queries, joining the warps), then one for each tile.  A CTA takes the tiles that lie
+// in its run.  Without the cost, runs over short sequences take longest: 64 sequences of 129
+// to 8192 tokens took 64 us with none, 52 with 16, 47 with 40 or 48, 50 with 64; 48
+// sequences of 5 to 300 took 11.3 us with 16, 12.7 with 40.  Lengths that cannot be are taken as 0.
+constexpr int kItemCost = 40;
 __device__ __forceinline__ int attend_len(const KvView& c, const AttendArgs& a, int b) {
   const int len = a.lens[b];
   return len < 0 || len > a.max_len || len > c.width * c.tiles_per_page * kTileTok ? -1 : len;
@@ -222,7 +223,11 @@ struct AttendSmem {
   static constexpr int kMergeWarps = NT == 1 ? kAW : kAW / 2;
   static constexpr int kBars = kRing + kMergeWarps * 32 * kFrag * 4;
   static constexpr int kWalk = kBars + kAW * kStages * 8;  // two walks a warp: kept here between uses, not in registers
-  static constexpr int kTmp = kWalk + kAW * 2 * (int)sizeof(Walk);
+  // prepared queries of a segment: fragments [NT][NB][32 lanes] of 16 bytes, the base's parts
+  // [NT][32 lanes] of 8 bytes, scales [8 NT]
+  static constexpr int kQuery = (kWalk + kAW * 2 * (int)sizeof(Walk) + 15) / 16 * 16;
+  static constexpr int kParts = kQuery + NT * (D / 32) * 512, kScale = kParts + NT * 256;
+  static constexpr int kTmp = kScale + 32 * NT;
   static constexpr int kPre = kTmp + 64;
   static int bytes(int n_seqs) { return kPre + (n_seqs + 1) * 4; }
 };
@@ -307,86 +312,96 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
     }
     turn = min(turn + 1, held);
   };
-#pragma unroll
-  for (int s = 0; s < ST; ++s) issue(s);
-
   int stage = 0;
   uint32_t phase = 0;
-  bool alive = true;
+  bool alive = true, first = true;
   while (walks[0].more) {
     const Segment sg = walks[0].s;
     const int h = sg.item / a.n_chunks, chunk = sg.item - h * a.n_chunks;
     const int n_heads = min(COLS, a.group - chunk * COLS);  // query heads of this item
     const int h0 = h * a.group + chunk * COLS;
-    // Query fragments: column n = g of each 8 heads; within a block the channels of the two
-    // 16-deep steps are 4t + {0, 2, 1, 3} and 16 more, the order that the nibbles come in.
-    uint32_t qf[NT][NB][4];
-    // -72 times the sum of a block's channels in three parts; a lane's rows of the product are
-    // blocks 2 (t mod 2), + 1 (t < 2: first part and third, else second), as its scales lie.
-    uint32_t qb[NT][2];
-    float sc[NT][2];      // their scale, with the power of two that the queries were divided by
+    // Queries, prepared once for the CTA: warp w takes heads w, w + 8 of the item, a lane
+    // D / 32 consecutive channels (8 or 16 lanes to a block).  As fragments column n = g of
+    // each 8 heads; within a block the channels of the two 16-deep steps are 4t + {0, 2, 1, 3}
+    // and 16 more, the order that the nibbles come in.
+    constexpr int C = D / 32;
+    __align__(8) uint16_t raw[NT][C];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const bool has = n * 8 + g < n_heads;
-      const T* qp = static_cast<const T*>(a.q) + sg.b * a.q_seq + (int64_t)(h0 + n * 8 + (has ? g : 0)) * a.q_head + 4 * t;
-      uint16_t e[NB][2][4] = {};
-      if (has) {
+      const bool has = n * 8 + warp < n_heads;
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sg.b * a.q_seq + (int64_t)(h0 + n * 8 + (has ? warp : 0)) * a.q_head + C * lane;
+      if (a.vec) {
+        if constexpr (C == 4) *reinterpret_cast<uint2*>(raw[n]) = *reinterpret_cast<const uint2*>(qp);
+        else *reinterpret_cast<uint32_t*>(raw[n]) = *reinterpret_cast<const uint32_t*>(qp);
+      } else {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint16_t* at = reinterpret_cast<const uint16_t*>(qp + nb * 32 + hf * 16);
-            if (a.vec) {
-              *reinterpret_cast<uint2*>(e[nb][hf]) = *reinterpret_cast<const uint2*>(at);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) e[nb][hf][i] = at[i];
-            }
-          }
+        for (int i = 0; i < C; ++i) raw[n][i] = qp[i];
       }
-      float top = 0.0f;
+    }
+    if (first) {  // the first pages are looked up and asked for while the queries come
+#pragma unroll 1
+      for (int s = 0; s < ST; ++s) issue(s);
+      first = false;
+    }
 #pragma unroll
-      for (int i = 0; i < NB * 8; ++i) top = fmaxf(top, fabsf(to_float(reinterpret_cast<const T*>(e)[i])));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    for (int n = 0; n < NT; ++n) {
+      const bool has = n * 8 + warp < n_heads;
+      float v[C], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        v[i] = has ? to_float(reinterpret_cast<const T*>(raw[n])[i]) : 0.0f;
+        top = fmaxf(top, fabsf(v[i]));
+      }
+#pragma unroll
+      for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       // 2^-x and 2^x, x the exponent of the largest channel (0 for none, infinity or NaN)
       int x = (int)(__float_as_uint(top) >> 23) - 127;
       if (top == 0.0f || x > 127) x = 0;
       x = max(min(x, 126), -60);  // smaller queries are 0 to any product
-      const float down = __uint_as_float((uint32_t)(127 - x) << 23), up = a.scale2 * exp2f((float)x);
-      sc[n][0] = __shfl_sync(0xffffffffu, up, 8 * t);
-      sc[n][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
-      float base_sum[NB];
+      const float down = __uint_as_float((uint32_t)(127 - x) << 23);
+      float sum = 0.0f;
+      uint16_t* frag = reinterpret_cast<uint16_t*>(sm + S::kQuery);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float sum = 0.0f;
+      for (int i = 0; i < C; ++i) {
+        const __half r = __float2half_rn(v[i] * down);
+        sum += __half2float(r);
+        // channel c of a block: lane t = (c mod 16) / 4, its word 2 [c >= 16] + [c odd], half [c mod 4 >= 2]
+        const int ch = C * lane + i, cc = ch & 31;
+        frag[((n * NB + (ch >> 5)) * 32 + warp * 4 + ((cc & 15) >> 2)) * 8 + ((cc >> 4) * 2 + (cc & 1)) * 2 + ((cc >> 1) & 1)] =
+            __half_as_ushort(r);
+      }
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          __half r[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            r[i] = __float2half_rn(to_float(reinterpret_cast<const T*>(e[nb][hf])[i]) * down);
-            sum += __half2float(r[i]);
-          }
-          qf[n][nb][2 * hf] = __half_as_ushort(r[0]) | (uint32_t)__half_as_ushort(r[2]) << 16;
-          qf[n][nb][2 * hf + 1] = __half_as_ushort(r[1]) | (uint32_t)__half_as_ushort(r[3]) << 16;
+      for (int off = 1; off < 32 / C; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      // -72 times the sum of a block's channels in three parts.  Lane t of a column's four has
+      // rows 2t, 2t + 1 and 2t + 8, 2t + 9 of that product: blocks 2 (t mod 2), + 1, as its scales lie; the first part in
+      // lanes 0 and 1, the second in 2 and 3, the third in the later rows of 0 and 1.
+      if (lane % (32 / C) == 0) {
+        const int nb = lane / (32 / C);
+        const float base = sum * -72.0f;
+        const __half p1 = __float2half_rn(base), p2 = __float2half_rn(base - __half2float(p1));
+        const __half p3 = __float2half_rn(base - __half2float(p1) - __half2float(p2));
+        __half* pt = reinterpret_cast<__half*>(sm + S::kParts) + (n * 32 + warp * 4) * 4;  // [t][2 words][2 blocks]
+        const int t0 = nb >> 1, i = nb & 1;
+        pt[t0 * 4 + i] = p1;
+        pt[(t0 + 2) * 4 + i] = p2;
+        pt[t0 * 4 + 2 + i] = p3;
+        pt[(t0 + 2) * 4 + 2 + i] = __half(0);
+        if (NB == 2) {  // two blocks: the odd lanes have none
+          pt[4 + i] = pt[6 + i] = pt[12 + i] = pt[14 + i] = __half(0);
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        base_sum[nb] = sum * -72.0f;
       }
-      uint16_t part[2][2];  // this lane's two blocks: [first or second part, third part or nothing]
+      if (lane == 0) reinterpret_cast<float*>(sm + S::kScale)[n * 8 + warp] = a.scale2 * exp2f((float)x);
+    }
+    __syncthreads();
+    uint32_t qf[NT][NB][4], qb[NT][2];
+    float sc[NT][2];  // scale of columns 2t and 2t + 1, with the power of two that the queries were divided by
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float v = NB == 4 && (t & 1) ? base_sum[(2 + i) % NB] : base_sum[i];
-        const __half p1 = __float2half_rn(v), p2 = __float2half_rn(v - __half2float(p1));
-        const __half p3 = __float2half_rn(v - __half2float(p1) - __half2float(p2));
-        const bool twice = NB == 2 && (t & 1);  // two blocks: lanes 0 and 2 alone
-        part[0][i] = twice ? 0 : __half_as_ushort(t < 2 ? p1 : p2);
-        part[1][i] = twice || t >= 2 ? 0 : __half_as_ushort(p3);
-      }
-      qb[n][0] = part[0][0] | (uint32_t)part[0][1] << 16;
-      qb[n][1] = part[1][0] | (uint32_t)part[1][1] << 16;
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        *reinterpret_cast<uint4*>(qf[n][nb]) = reinterpret_cast<const uint4*>(sm + S::kQuery)[(n * NB + nb) * 32 + lane];
+      *reinterpret_cast<uint2*>(qb[n]) = reinterpret_cast<const uint2*>(sm + S::kParts)[n * 32 + lane];
+      *reinterpret_cast<float2*>(sc[n]) = reinterpret_cast<const float2*>(sm + S::kScale)[n * 4 + t];
     }
     float o[NT][NB][2][4];
     float m[NT][2], l[NT][2];  // m in units of the unscaled products
@@ -642,6 +657,10 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
     }
     __syncthreads();
     const bool whole = walks[0].s.s0 == 0 && walks[0].s.s1 == walks[0].s.nt;
+    if (tid == 0 && sg.s0 == 0) {
+      const int end = pre[sg.b] * items + (sg.item + 1) * (sg.nt + kItemCost) - 1;
+      a.pieces[sg.b * items + sg.item] = make_int2(blockIdx.x, end / run - (int)blockIdx.x + 1);
+    }
     const int slot = 2 * blockIdx.x + (sg.s0 == 0 ? 1 : 0);
     const int e4 = warp & 3, e = e4 & 1;
 #pragma unroll
@@ -692,47 +711,94 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 
 // ------------------------------------------------------------------ second kernel
 
-// CTA x < items * 8 NT joins the partial results of one head of an item (or writes the row of
-// a sequence without positions: zeros, or NaN when its length cannot be): the pieces'
-// weights are formed once, one thread each, then every thread sums its channel (the
-// pieces in 256 / D interleaved lines, so that loads are in flight together).  Scored
-// calls then add the weights of keys to the caller's scores, 256 keys of a sequence
+// The first CTAs join the partial results of items (or write the rows of a sequence without
+// positions: zeros, or NaN when its length cannot be).  With few items (each in many pieces)
+// a CTA takes one head: the pieces' weights are formed once, one thread each, then every thread
+// sums its channel, the pieces in kJoinThreads / D interleaved lines, eight loads in flight.
+// With many items (most of them whole or in two pieces) a CTA takes all heads of an item, so that there are
+// few CTAs to start.  Scored
+// calls then add the weights of keys to the caller's scores, kJoinThreads keys of a sequence
 // and KV head a CTA.  A position's weight is summed over its heads in order by one thread: no
 // atomics.
 constexpr int kJoinMax = 1024;  // most pieces of an item: one per CTA of the first kernel
+constexpr int kJoinThreads = 512;
+
+// (m, l) of one column of an item over its pieces, by one thread.
+__device__ __forceinline__ void join_ml(const AttendArgs& a, int item, int cols, int col, float* m_out, float* l_out) {
+  const int2 pc = a.pieces[item];
+  if (pc.y == 1) {
+    const float2 ml = reinterpret_cast<const float2*>(a.ml_whole)[(int64_t)item * cols + col];
+    *m_out = ml.x;
+    *l_out = ml.y;
+    return;
+  }
+  float M = -INFINITY, L = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < pc.y; ++k) {
+    const float2 ml = reinterpret_cast<const float2*>(a.ml)[(2 * (int64_t)(pc.x + k) + (k == 0 ? 1 : 0)) * cols + col];
+    const float mn = fmaxf(M, ml.x);
+    L = L * (M == mn ? 1.0f : exp2_fast(M - mn)) + ml.y * (ml.x == mn ? 1.0f : exp2_fast(ml.x - mn));
+    M = mn;
+  }
+  *m_out = M;
+  *l_out = L;
+}
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const AttendArgs a, int n_cta) {
-  constexpr int COLS = 8 * NT, WAYS = 256 / D;
-  __shared__ int tmp[8];
-  __shared__ float sm_m[kJoinMax], sm_l[kJoinMax];  // per head of a KV head's chunks; pieces of an item
-  __shared__ float red[256];
-  extern __shared__ int pre[];
+__global__ void __launch_bounds__(kJoinThreads) kv_attend_join(const KvView c, const AttendArgs a) {
+  constexpr int COLS = 8 * NT, WAYS = kJoinThreads / D;
+  __shared__ float sm_m[kJoinMax], sm_l[kJoinMax];  // pieces of an item; heads of a KV head
+  __shared__ float red[kJoinThreads], red_l[WAYS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  attend_prefix(c, a, pre, tmp);
-  const int items = c.heads * a.n_chunks;
-  const int total = pre[c.n_seqs] * items;
-  const int run = attend_run(a, total, n_cta);
-  const int all = c.n_seqs * items;
+  const int items = c.heads * a.n_chunks, all = c.n_seqs * items;
+  const int n_join = all * (COLS / a.join_cols);
+  const bool joins = (int)blockIdx.x < n_join;
+  const int per = (a.max_len + kJoinThreads - 1) / kJoinThreads;
+  const int x = (int)blockIdx.x - n_join;
+  const int idx = joins ? blockIdx.x / (COLS / a.join_cols) : 0;
+  const int b = joins ? idx / items : x / per / c.heads;
+  const int len = attend_len(c, a, b);  // an argument of the call: not written by the first kernel
   // Every CTA waits for the first kernel, also one without work: this grid's end stands for both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x < all * COLS) {
-    const int col = blockIdx.x % COLS, idx = blockIdx.x / COLS;
-    const int b = idx / items, item = idx % items;
+  if (joins) {
+    const int col = a.join_cols == 1 ? blockIdx.x % COLS : 0, item = idx % items;
     const int h = item / a.n_chunks, chunk = item - h * a.n_chunks;
-    const int places = pre[b + 1] - pre[b];
-    if (col >= a.group - chunk * COLS) return;
+    const int n_heads = min(COLS, a.group - chunk * COLS);
+    if (col >= n_heads) return;
     T* out = static_cast<T*>(a.out) + b * a.o_seq + (int64_t)(h * a.group + chunk * COLS + col) * a.o_head;
-    if (places == 0) {
-      const bool bad = attend_len(c, a, b) < 0;
-      if (bad && tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
-      if (tid < D) out[tid] = from_float<T>(bad ? __int_as_float(0x7fc00000) : 0.0f);
+    if (len <= 0) {
+      if (len < 0 && tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
+      const int n = a.join_cols == 1 ? D : n_heads * D;
+      for (int o = tid; o < n; o += kJoinThreads)
+        out[(o / D) * a.o_head + o % D] = from_float<T>(len < 0 ? __int_as_float(0x7fc00000) : 0.0f);
       return;
     }
-    const int lo = pre[b] * items + item * places;
-    const int c0 = (lo + kItemCost) / run, n = (lo + places - 1) / run - c0 + 1;
+    if (a.join_cols != 1) {
+      const int2 pc = a.pieces[idx];
+      if (pc.y == 1) return;  // one CTA had it whole
+      for (int o = tid; o < n_heads * D; o += kJoinThreads) {
+        const int hc = o / D, ch = o % D;
+        float M = -INFINITY, L = 0.0f, O = 0.0f;
+#pragma unroll 2
+        for (int k = 0; k < pc.y; ++k) {
+          const int64_t at = (2 * (int64_t)(pc.x + k) + (k == 0 ? 1 : 0)) * COLS + hc;
+          const float2 ml = reinterpret_cast<const float2*>(a.ml)[at];
+          const float v = a.part[at * D + ch];
+          const float mn = fmaxf(M, ml.x);
+          const float fo = M == mn ? 1.0f : exp2_fast(M - mn), fk = ml.x == mn ? 1.0f : exp2_fast(ml.x - mn);
+          L = L * fo + ml.y * fk;
+          O = O * fo + v * fk;
+          M = mn;
+        }
+        out[hc * a.o_head + ch] = from_float<T>(L != L ? L : O / L);
+      }
+      return;
+    }
+    const int2 pc = a.pieces[idx];
+    const int c0 = pc.x, n = pc.y;
     if (n == 1) return;  // one CTA had it whole
     float m = -INFINITY;
-    for (int k = tid; k < n; k += 256) {
+    for (int k = tid; k < n; k += kJoinThreads) {
       const float2 ml = reinterpret_cast<const float2*>(a.ml)[(2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * COLS + col];
       sm_m[k] = ml.x;
       sm_l[k] = ml.y;
@@ -743,10 +809,10 @@ __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const Atte
     if (lane == 0) red[warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
     const int ch = tid % D, way = tid / D;
     float L = 0.0f, O = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = way; k < n; k += WAYS) {
       const float f = sm_m[k] == m ? 1.0f : exp2_fast(sm_m[k] - m);
       L = fmaf(sm_l[k], f, L);
@@ -754,41 +820,24 @@ __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const Atte
     }
     __syncthreads();
     red[tid] = O;
+    if (ch == 0) red_l[way] = L;
     __syncthreads();
-    float sum = 0.0f;
-    for (int w = 0; w < WAYS; ++w) sum += red[w * D + ch];
-    __syncthreads();
-    red[tid] = L;
-    __syncthreads();
-    float den = 0.0f;
-    for (int w = 0; w < WAYS; ++w) den += red[w * D + ch];
-    if (way == 0) out[ch] = from_float<T>(sum / den);  // a NaN of any piece's sum is in den
+    if (way) return;
+    float sum = 0.0f, den = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAYS; ++w) {
+      sum += red[w * D + ch];
+      den += red_l[w];
+    }
+    out[ch] = from_float<T>(sum / den);  // a NaN of any piece's sum is in den
     return;
   }
-  if (!a.score) return;
-  const int per = (a.max_len + 255) / 256;
-  const int x = blockIdx.x - all * COLS, bh = x / per, b = bh / c.heads, h = bh % c.heads;
-  const int places = pre[b + 1] - pre[b], len = attend_len(c, a, b);
-  const int key0 = (x % per) * 256;
+  const int h = x / per % c.heads;
+  const int key0 = (x % per) * kJoinThreads;
   if (key0 >= len) return;
-  for (int col = tid; col < a.n_chunks * COLS; col += 256) {
-    const int chunk = col / COLS, cc = col % COLS, item = h * a.n_chunks + chunk;
-    const int lo = pre[b] * items + item * places;
-    const int c0 = (lo + kItemCost) / run, c1 = (lo + places - 1) / run;
-    float M = -INFINITY, L = 0.0f;
-    if (c0 == c1) {
-      const float* ml = a.ml_whole + ((int64_t)(b * items + item) * COLS + cc) * 2;
-      M = ml[0];
-      L = ml[1];
-    } else {
-      for (int k = c0; k <= c1; ++k) {
-        const int64_t slot = 2 * (int64_t)k + (k == c0 ? 1 : 0);
-        const float mk = a.ml[(slot * COLS + cc) * 2], lk = a.ml[(slot * COLS + cc) * 2 + 1];
-        const float mn = fmaxf(M, mk);
-        L = L * (M == mn ? 1.0f : exp2_fast(M - mn)) + lk * (mk == mn ? 1.0f : exp2_fast(mk - mn));
-        M = mn;
-      }
-    }
+  for (int col = tid; col < a.n_chunks * COLS; col += kJoinThreads) {
+    float M, L;
+    join_ml(a, b * items + h * a.n_chunks + col / COLS, COLS, col % COLS, &M, &L);
     sm_m[col] = M;
     sm_l[col] = 1.0f / L;
   }
@@ -796,12 +845,19 @@ __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const Atte
   const int key = key0 + tid;
   if (key >= len) return;
   float w = 0.0f;
-  for (int head = 0; head < a.group; ++head) {
-    const int chunk = head / COLS, cc = head % COLS;
-    const float zz = a.z[((int64_t)(b * items + h * a.n_chunks + chunk) * a.max_len + key) * COLS + cc];
-    w += exp2_fast(zz - sm_m[head]) * sm_l[head];
+  const float* z = a.z + ((int64_t)(b * items + h * a.n_chunks) * a.max_len + key) * COLS;
+  float* score = a.score + b * a.s_seq + h * a.s_head + key;
+  const float old = *score;
+  for (int chunk = 0; chunk < a.n_chunks; ++chunk, z += (int64_t)a.max_len * COLS) {
+    const int n = min(COLS, a.group - chunk * COLS);
+    float4 v[COLS / 4];
+#pragma unroll
+    for (int i = 0; i < COLS / 4; ++i) v[i] = reinterpret_cast<const float4*>(z)[i];
+#pragma unroll
+    for (int i = 0; i < COLS; ++i)
+      if (i < n) w += exp2_fast(reinterpret_cast<const float*>(v)[i] - sm_m[chunk * COLS + i]) * sm_l[chunk * COLS + i];
   }
-  a.score[b * a.s_seq + h * a.s_head + key] += w;
+  *score = old + w;
 }
 
 // ------------------------------------------------------------------ host
@@ -809,7 +865,7 @@ __global__ void __launch_bounds__(256) kv_attend_join(const KvView c, const Atte
 struct AttendPlan {
   int nt, chunks, n_cta, min_run;
   int64_t items;
-  size_t part, ml, ml_whole, z, total;  // byte offsets
+  size_t part, ml, ml_whole, pieces, z, total;  // byte offsets
 };
 
 static int sm_count(int dev) {
@@ -831,7 +887,7 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   p->chunks = (group + 8 * p->nt - 1) / (8 * p->nt);
   p->items = (int64_t)c.n_seqs * c.heads * p->chunks;
   const int64_t tiles = p->items * ((max_len + kTileTok - 1) / kTileTok + kItemCost);
-  const int per = (max_len + 255) / 256;
+  const int per = (max_len + kJoinThreads - 1) / kJoinThreads;
   if (tiles > INT32_MAX / 2 || p->items * 8 * p->nt + (scored ? (int64_t)c.n_seqs * c.heads * per : 0) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const int sms = sm_count(device);
   if (!sms) return MOE_ERR_CUDA;
@@ -852,14 +908,14 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   p->part = take((size_t)2 * p->n_cta * cols * c.dim * 4);
   p->ml = take((size_t)2 * p->n_cta * cols * 8);
   p->ml_whole = take(scored ? (size_t)p->items * cols * 8 : 0);
+  p->pieces = take((size_t)p->items * 8);
   p->z = take(scored ? (size_t)p->items * max_len * cols * 4 : 0);
   p->total = off;
   return MOE_OK;
 }
 
-template <typename K>
-static cudaError_t launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st, bool dependent,
-                          const KvView& c, const AttendArgs& a, int n_cta) {
+static cudaError_t launch(void (*kernel)(const KvView, const AttendArgs), int grid, int threads, size_t smem,
+                          cudaStream_t st, bool dependent, const KvView& c, const AttendArgs& a) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -870,8 +926,7 @@ static cudaError_t launch(K kernel, int grid, int threads, size_t smem, cudaStre
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = dependent ? 1 : 0;
-  if constexpr (std::is_invocable_v<K, KvView, AttendArgs>) return cudaLaunchKernelEx(&cfg, kernel, c, a);
-  else return cudaLaunchKernelEx(&cfg, kernel, c, a, n_cta);
+  return cudaLaunchKernelEx(&cfg, kernel, c, a);
 }
 
 template <typename T, int D, int NT>
@@ -885,12 +940,12 @@ static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendP
     if (e != cudaSuccess) return e;
     ready[device] = true;
   }
-  cudaError_t e = a.score ? launch(kv_attend_kernel<T, D, NT, true>, p.n_cta, kAW * 32, smem, st, false, c, a, 0)
-                          : launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a, 0);
+  cudaError_t e = a.score ? launch(kv_attend_kernel<T, D, NT, true>, p.n_cta, kAW * 32, smem, st, false, c, a)
+                          : launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a);
   if (e != cudaSuccess) return e;
-  const int per = (a.max_len + 255) / 256;
-  const int grid = (int)p.items * 8 * NT + (a.score ? c.n_seqs * c.heads * per : 0);
-  return launch(kv_attend_join<T, D, NT>, grid, 256, (size_t)(c.n_seqs + 1) * 4, st, true, c, a, p.n_cta);
+  const int per = (a.max_len + kJoinThreads - 1) / kJoinThreads;
+  const int grid = (int)p.items * (8 * NT / a.join_cols) + (a.score ? c.n_seqs * c.heads * per : 0);
+  return launch(kv_attend_join<T, D, NT>, grid, kJoinThreads, 0, st, true, c, a);
 }
 
 }  // namespace moe
@@ -938,10 +993,12 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   a.n_chunks = p.chunks;
   a.scale2 = scale * 1.4426950408889634f;
   a.min_run = p.min_run;
+  a.join_cols = p.items < 64 ? 1 : 8 * p.nt;
   a.vec = kv_align_ok(q->data_dev, 8) && q->token_stride % 4 == 0 && q->head_stride % 4 == 0;
   a.part = reinterpret_cast<float*>(ws + p.part);
   a.ml = reinterpret_cast<float*>(ws + p.ml);
   a.ml_whole = reinterpret_cast<float*>(ws + p.ml_whole);
+  a.pieces = reinterpret_cast<int2*>(ws + p.pieces);
   a.z = reinterpret_cast<float*>(ws + p.z);
   if (score) {
     a.score = score->data_dev;
