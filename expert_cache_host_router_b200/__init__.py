@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import atexit
 import ctypes
-import functools
 import os
 import re
 import weakref
@@ -415,121 +414,51 @@ class ExpertCacheMoE:
 
 # ------------------------------------------------------------------ attention operators
 #
-# These calls are made once per layer and token, so the checks below build their messages
-# only when they fail.
+# torch tensors in, torch tensors out, on the current stream of the tensors' device or on
+# `stream`.  These calls are made once per layer and token, so their arguments are checked
+# and converted in an extension module (csrc/bind.cpp) that calls the C ABI.
 
-_torch = None  # torch, imported by the first call; with it _DT and the types the checks compare with
-_DT = {}
+BIND_PATH = os.path.join(_PKG, "_lib", "_moe_bind.so")
+_bind_module = None
 
 
-def _load_torch():
-    global _torch
+def _bind():
+    """Load _moe_bind.so (built in-tree by expert_cache_host_router_b200.build)."""
+    global _bind_module
+    if _bind_module is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module is linked to its libraries)
+        if not os.path.exists(BIND_PATH):
+            raise ImportError(f"_moe_bind.so not built ({BIND_PATH}); run expert_cache_host_router_b200/build.py")
+        lib()
+        loader = importlib.machinery.ExtensionFileLoader("_moe_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_moe_bind", loader))
+        loader.exec_module(module)
+        module.set_error(MoEError)
+        _bind_module = module
+    return _bind_module
+
+
+def _on(stream, tensor):
+    """The given stream as the current one (buffers made in the call then belong to it)."""
     import torch
-    _DT.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32})
-    _torch = torch
-    return torch
-
-
-def _refuse(what: str):
-    raise MoEError(MOE_ERR_INVALID, what)
-
-
-def _ints(t, dim: int, dev, what: str, n=None) -> int:
-    if t.dtype != _torch.int32 or t.dim() != dim or t.device != dev or (n is not None and t.shape[0] != n) \
-            or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        _refuse(f"{what} must be an int32 tensor of {dim} dimension(s){'' if n is None else f' and {n} entries'} on {dev}, "
-                "its last one contiguous")
-    return t.data_ptr()
-
-
-def _kv_pool(pool, error, what: str):
-    if _torch is None:
-        _load_torch()
-    if pool.dtype != _torch.uint8 or pool.dim() != 4 or not pool.is_cuda or not pool.is_contiguous() or pool.shape[3] % 18:
-        _refuse(f"{what}: pool must be a contiguous uint8 CUDA tensor [pages, KV heads, page tokens / 16, 18 * head dim]")
-    pages, heads, tiles, size = pool.shape
-    dev = pool.device
-    return dev, KvPool(pool.data_ptr(), pages, heads, size // 18, tiles * 16, dev.index,
-                       None if error is None else _ints(error, 1, dev, what + ": error"))
-
-
-def _kv_table(table, dev, what: str):
-    p = _ints(table, 2, dev, what)
-    n, w = table.shape
-    return KvTable(p, n, w, table.stride(0) if n > 1 else w)
-
-
-def _rows(t, n, heads, dim, dtype, dev, what: str):
-    if t.shape != (n, heads, dim) or t.dtype != dtype or t.device != dev or t.stride(2) != 1:
-        _refuse(f"{what} must be a {dtype} tensor {[n, heads, dim]} on {dev}, its last dimension contiguous")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _kv_score(score, n, heads, most, dev, what: str):
-    if score.dtype != _torch.float32 or score.dim() != 3 or score.shape[0] != n or score.shape[1] != heads \
-            or score.shape[2] < most or score.device != dev or (score.shape[2] > 1 and score.stride(2) != 1):
-        _refuse(f"{what} must be a float32 tensor [{n}, {heads}, >= {most}] on {dev}, its last dimension contiguous")
-    return KvScore(score.data_ptr(), score.stride(0), score.stride(1))
-
-
-def _dtype(t, what: str) -> int:
-    d = _DT.get(t)
-    return _refuse(f"{what}: dtype {t}") if d is None else d
-
-
-def _stream(stream, dev) -> int:
-    """Handle of the stream to launch on (the current one of the tensors' device without `stream`)."""
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev.index)
-    if stream.device != dev:
-        _refuse(f"the stream is on {stream.device}, the tensors are on {dev}")
-    return stream.cuda_stream
-
-
-def _empty(stream, shape, dtype, dev):
-    """A buffer that belongs to the stream that the call runs on."""
-    if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=dev)
-    with _torch.cuda.stream(stream):
-        return _torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _like(stream, t):
-    """The same for a tensor like t (dense, the last dimension contiguous as t's is)."""
-    if stream is None:
-        return _torch.empty_like(t)
-    with _torch.cuda.stream(stream):
-        return _torch.empty_like(t)
+    if tensor.device != stream.device:
+        raise MoEError(MOE_ERR_INVALID, f"the stream is on {stream.device}, the tensors are on {tensor.device}")
+    return torch.cuda.stream(stream)
 
 
 def kv_pool(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device=0):
     """A zeroed 4-bit key/value cache: uint8 [n_pages, n_kv_heads, page_tokens / 16, 18 * head_dim]
     (page_tokens a multiple of 16, head_dim 64 or 128; layout in include/moe_cache.h)."""
-    torch = _torch or _load_torch()
+    import torch
     if page_tokens < 16 or page_tokens % 16:
-        _refuse(f"kv_pool: page_tokens {page_tokens} is not a multiple of 16")
+        raise MoEError(MOE_ERR_INVALID, f"kv_pool: page_tokens {page_tokens} is not a multiple of 16")
     if head_dim not in (64, 128):
-        _refuse(f"kv_pool: head_dim {head_dim} is neither 64 nor 128")
+        raise MoEError(MOE_ERR_INVALID, f"kv_pool: head_dim {head_dim} is neither 64 nor 128")
     return torch.zeros((n_pages, n_kv_heads, page_tokens // 16, 18 * head_dim), dtype=torch.uint8,
                        device=torch.device("cuda", device) if isinstance(device, int) else device)
-
-
-def _kv_rows_call(call, name, dev, c, k, v, made, table, cu, start, n, stream):
-    t = _kv_table(table, dev, name + ": table")
-    b, heads, dim, dt = t.n_seqs, c.n_kv_heads, c.head_dim, k.dtype
-    cu_p = _ints(cu, 1, dev, name + ": cu", b + 1)
-    start_p = None if start is None else _ints(start, 1, dev, name + ": start", b)
-    if made:  # rows that were made here
-        rk, rv = Rows(k.data_ptr(), heads * dim, dim), Rows(v.data_ptr(), heads * dim, dim)
-    else:
-        rk = _rows(k, n, heads, dim, dt, dev, name + ": k")
-        rv = _rows(v, n, heads, dim, dt, dev, name + ": v")
-    d = _dtype(dt, name)
-    s = _stream(stream, dev)
-    if n and b:
-        st = call(c, t, cu_p, start_p, rk, rv, n, d, s)
-        if st:
-            raise MoEError(st, "moe_" + name)
 
 
 def kv_store(pool, k, v, table, cu, start=None, error=None, stream=None) -> None:
@@ -537,32 +466,22 @@ def kv_store(pool, k, v, table, cu, start=None, error=None, stream=None) -> None
     rows cu[b] .. cu[b + 1] - 1 go to positions start[b] .. (0 .. without start) of sequence
     b, whose pages are table[b].  Rows outside cu[0] .. cu[-1] are padding.  error: int32
     [1], receives MOE_DEVERR_PAGE when a row has no place in the cache (that row is skipped)."""
-    dev, c = _kv_pool(pool, error, "kv_store")
-    _kv_rows_call(lib().moe_kv_store, "kv_store", dev, c, k, v, False, table, cu, start, k.shape[0], stream)
+    f = (_bind_module or _bind()).kv_store
+    if stream is None:
+        return f(pool, k, v, table, cu, start, error)
+    with _on(stream, pool):
+        return f(pool, k, v, table, cu, start, error)
 
 
 def kv_load(pool, table, cu, start, n_tokens: int, dtype, out=None, error=None, stream=None):
     """Read cached rows back as the values they stand for, addressed as in kv_store.  Returns
     (k, v) [n_tokens, KV heads, head dim]; out: that pair of tensors to write to.  Padding
     rows are left as they were (unspecified in tensors made here)."""
-    dev, c = _kv_pool(pool, error, "kv_load")
-    made = out is None
-    if made:
-        k = _empty(stream, (n_tokens, c.n_kv_heads, c.head_dim), dtype, dev)
-        out = k, _like(stream, k)
-    elif out[0].dtype != dtype:
-        _refuse(f"kv_load: out must be {dtype}")
-    _kv_rows_call(lib().moe_kv_load, "kv_load", dev, c, out[0], out[1], made, table, cu, start, n_tokens, stream)
-    return out
-
-
-@functools.lru_cache(maxsize=256)
-def _attend_workspace(heads, dim, page, device, n_seqs, width, n_q_heads, max_len, scored) -> int:
-    n = ctypes.c_size_t(0)
-    # sizes alone: the addresses only have to be non-null and aligned
-    _check(lib().moe_kv_attend_workspace(KvPool(256, 1, heads, dim, page, device, None), KvTable(256, n_seqs, width, width),
-                                         n_q_heads, max_len, scored, n), "moe_kv_attend_workspace")
-    return n.value
+    f = (_bind_module or _bind()).kv_load
+    if stream is None:
+        return f(pool, table, cu, start, n_tokens, dtype, out, error)
+    with _on(stream, pool):
+        return f(pool, table, cu, start, n_tokens, dtype, out, error)
 
 
 def kv_attend(pool, q, table, lens, max_len=None, scale=None, score=None, out=None, workspace=None, error=None,
@@ -571,48 +490,20 @@ def kv_attend(pool, q, table, lens, max_len=None, scale=None, score=None, out=No
     fp16), over the first lens[b] cached positions of each.  max_len: an upper bound of lens
     known here (default: all that table holds); scale: default head_dim ** -0.5.  score:
     float32 [sequences, KV heads, >= max_len], to which every position's weight, summed
-    over the query heads of its KV head, is added.  workspace: uint8 tensor of at least
+    over the query heads of its KV head, is added.  workspace: contiguous tensor of at least
     kv_attend_workspace(...) bytes for callers that keep their own; made here otherwise.
     Returns out (q's shape and type); a sequence of length 0 gives zeros, one whose length
     or pages lie outside the cache NaN (and error, int32 [1], MOE_DEVERR_PAGE)."""
-    dev, c = _kv_pool(pool, error, "kv_attend")
-    t = _kv_table(table, dev, "kv_attend: table")
-    n, dim, dt = t.n_seqs, c.head_dim, q.dtype
-    lens_p = _ints(lens, 1, dev, "kv_attend: lens", n)
-    if q.dim() != 3:
-        _refuse("kv_attend: q must have three dimensions")
-    heads = q.shape[1]
-    most = t.width * c.page_tokens if max_len is None else max_len
-    rq = _rows(q, n, heads, dim, dt, dev, "kv_attend: q")
-    sc = None if score is None else _kv_score(score, n, c.n_kv_heads, most, dev, "kv_attend: score")
-    d = _dtype(dt, "kv_attend")
-    s = _stream(stream, dev)
-    if out is None:
-        out = _like(stream, q)
-        ro = Rows(out.data_ptr(), out.stride(0), out.stride(1))
-    else:
-        ro = _rows(out, n, heads, dim, dt, dev, "kv_attend: out")
-    if not n:
-        return out
-    if workspace is None:
-        size = _attend_workspace(c.n_kv_heads, dim, c.page_tokens, c.device, n, t.width, heads, most, score is not None)
-        workspace = _empty(stream, size, _torch.uint8, dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        _refuse(f"kv_attend: workspace must be contiguous on {dev}")
-    else:
-        size = workspace.numel() * workspace.element_size()
-    st = lib().moe_kv_attend(c, t, lens_p, most, rq, heads, d, dim ** -0.5 if scale is None else scale, ro, sc,
-                             workspace.data_ptr(), size, s)
-    if st:
-        raise MoEError(st, "moe_kv_attend")
-    return out
+    f = (_bind_module or _bind()).kv_attend
+    if stream is None:
+        return f(pool, q, table, lens, max_len, scale, score, out, workspace, error)
+    with _on(stream, pool):
+        return f(pool, q, table, lens, max_len, scale, score, out, workspace, error)
 
 
 def kv_attend_workspace(pool, table, n_q_heads: int, max_len: int, scored: bool = False) -> int:
     """Bytes of workspace that kv_attend needs for these sizes."""
-    dev, c = _kv_pool(pool, None, "kv_attend_workspace")
-    return _attend_workspace(c.n_kv_heads, c.head_dim, c.page_tokens, c.device, table.shape[0], table.shape[1], n_q_heads,
-                             max_len, bool(scored))
+    return (_bind_module or _bind()).kv_attend_workspace(pool, table, n_q_heads, max_len, scored)
 
 
 def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out_table, error=None, stream=None):
@@ -621,23 +512,11 @@ def kv_evict(pool, table, lens, max_len: int, score, keep: int, recent: int, out
     copied in order to the pages of out_table (pages that table does not name).  Returns
     (lengths int32 [sequences], former positions int32 [sequences, KV heads, keep], scores
     float32 of the same shape); behind a sequence's end positions are -1, scores 0."""
-    dev, c = _kv_pool(pool, error, "kv_evict")
-    t, o = _kv_table(table, dev, "kv_evict: table"), _kv_table(out_table, dev, "kv_evict: out_table")
-    n, heads = t.n_seqs, c.n_kv_heads
-    lens_p = _ints(lens, 1, dev, "kv_evict: lens", n)
-    sc = _kv_score(score, n, heads, max_len, dev, "kv_evict: score")
-    if keep < 1:
-        _refuse(f"kv_evict: keep {keep}")
-    s = _stream(stream, dev)
-    out_lens = _empty(stream, (n,), _torch.int32, dev)
-    out_score = _empty(stream, (n, heads, keep), _torch.float32, dev)
-    kept = _empty(stream, (n, heads, keep), _torch.int32, dev)
-    if n:
-        st = lib().moe_kv_evict(c, t, lens_p, max_len, sc, keep, recent, o, out_lens.data_ptr(), kept.data_ptr(),
-                                out_score.data_ptr(), s)
-        if st:
-            raise MoEError(st, "moe_kv_evict")
-    return out_lens, kept, out_score
+    f = (_bind_module or _bind()).kv_evict
+    if stream is None:
+        return f(pool, table, lens, max_len, score, keep, recent, out_table, error)
+    with _on(stream, pool):
+        return f(pool, table, lens, max_len, score, keep, recent, out_table, error)
 
 
 def attend_prompt(q, k, v, cu, scale=None, out=None, error=None, stream=None):
@@ -646,30 +525,8 @@ def attend_prompt(q, k, v, cu, scale=None, out=None, error=None, stream=None):
     [sequences + 1]).  scale: default head_dim ** -0.5.  Returns out (q's shape and type);
     rows outside every sequence are left as they were (unspecified in a tensor made here).
     error: int32 [1], MOE_DEVERR_PAGE when a sequence's bounds are outside the rows."""
-    if _torch is None:
-        _load_torch()
-    if not q.is_cuda or q.dim() != 3 or k.dim() != 3:
-        _refuse("attend_prompt: q, k and v must be CUDA tensors of three dimensions")
-    dev, dt = q.device, q.dtype
-    n, heads, dim = q.shape
-    kv = k.shape[1]
-    rq = _rows(q, n, heads, dim, dt, dev, "attend_prompt: q")
-    rk = _rows(k, n, kv, dim, dt, dev, "attend_prompt: k")
-    rv = _rows(v, n, kv, dim, dt, dev, "attend_prompt: v")
-    cu_p = _ints(cu, 1, dev, "attend_prompt: cu")
-    if cu.shape[0] < 1:
-        _refuse("attend_prompt: cu is empty")
-    err = None if error is None else _ints(error, 1, dev, "attend_prompt: error")
-    d = _dtype(dt, "attend_prompt")
-    s = _stream(stream, dev)
-    if out is None:
-        out = _like(stream, q)
-        ro = Rows(out.data_ptr(), out.stride(0), out.stride(1))
-    else:
-        ro = _rows(out, n, heads, dim, dt, dev, "attend_prompt: out")
-    if n:
-        st = lib().moe_attend_prompt(dev.index, rq, rk, rv, ro, cu_p, cu.shape[0] - 1, n, heads, kv, dim, d,
-                                     dim ** -0.5 if scale is None else scale, err, s)
-        if st:
-            raise MoEError(st, "moe_attend_prompt")
-    return out
+    f = (_bind_module or _bind()).attend_prompt
+    if stream is None:
+        return f(q, k, v, cu, scale, out, error)
+    with _on(stream, q):
+        return f(q, k, v, cu, scale, out, error)

@@ -1,4 +1,5 @@
-"""Build libmoe.so (the CUDA library behind include/moe_cache.h) in-tree for sm_100a."""
+"""Build libmoe.so (the CUDA library behind include/moe_cache.h) in-tree for sm_100a, and the
+extension module that marshals torch tensors for its attention operators."""
 from __future__ import annotations
 
 import glob
@@ -11,6 +12,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmoe.so")
+BIND = os.path.join(OUT_DIR, "_moe_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -29,9 +32,32 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_bind(force: bool) -> None:
+    deps = [BIND_SRC, os.path.join(ROOT, "include", "moe_cache.h")]
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(d) for d in deps):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    inc = include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+                             os.path.join(ROOT, "include")]
+    tmp = BIND + f".{os.getpid()}.tmp"
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_moe_bind",
+                           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                           *[f"-I{i}" for i in inc], BIND_SRC, "-o", tmp, *[f"-L{p}" for p in library_paths()], f"-L{OUT_DIR}",
+                           "-l:libmoe.so", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+    if force or _stale():
+        _build_lib(verbose)
+    _build_bind(force)
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     os.makedirs(OUT_DIR, exist_ok=True)
     objs = []
     for src in sources():
@@ -46,7 +72,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     for o in objs:
         os.remove(o)
-    return LIB
 
 
 if __name__ == "__main__":

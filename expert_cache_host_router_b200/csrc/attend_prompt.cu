@@ -8,7 +8,7 @@
 // rows x 128 keys take 2048 cycles of tensor pipe (D = 128) and 2048 cycles of the
 // exponential unit (16 per cycle and SM), so both have to run at the same time.
 //
-// One CTA takes 256 query rows of one head as two tiles of 128, whose softmax and products
+// Work item: 256 query rows of one head, as two tiles of 128 whose softmax and products
 // alternate: while one tile's weights are formed, the tensor pipe works for the other.
 // Warp roles, joined by mbarriers:
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns a row; it reads S from tensor
@@ -17,6 +17,9 @@
 //   warp 8            TMA of Q, then of K and V tiles (128 keys) into a ring
 //   warp 9            tcgen05.mma of S, both operands from shared memory
 //   warp 10           tcgen05.mma of O, P from tensor memory and V from shared memory
+//   warp 11           which item comes next
+// The kernel is persistent, one CTA per SM: the next item's queries, keys and first products
+// come while the last one's output is written, and items go out longest first.
 // The maximum that a row's exponents refer to moves only when it is exceeded by more than
 // 2^8, so most key tiles rescale nothing; P stays below 256, inside either 16-bit type.
 // P is rounded to the input type (half a step per weight); sums, S and O are fp32.
@@ -181,6 +184,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 256 query rows of one head.
+struct PromptItem {
+  int row0, n, block, head;  // first row and rows of the sequence, number of the 256 rows in it
+  // key tiles of query tile w: up to the one on the diagonal; none for a second tile without rows
+  __device__ __forceinline__ int tiles(int w) const {
+    const int t = 2 * block + 1 + w;
+    return w && t > (n + kPN - 1) / kPN ? 0 : t;
+  }
+};
+
+// Blocks of 256 rows of sequence b, its first row and its rows; none if its bounds cannot be.
+__device__ __forceinline__ int prompt_blocks(const PromptArgs& a, int b, int* row, int* rows) {
+  *row = *rows = 0;
+  if (b >= a.n_seqs) return 0;
+  const int s = a.cu[b], n = a.cu[b + 1] - s;
+  if (s < 0 || n < 0 || n > a.n_tokens - s) {
+    kv_flag(a.error, MOE_DEVERR_PAGE);
+    return 0;
+  }
+  *row = s;
+  *rows = n;
+  return (n + 2 * kPM - 1) / (2 * kPM);
+}
+
 template <int D>
 struct PromptSmem {
   static constexpr int kStages = D == 64 ? 4 : 2;
@@ -211,28 +238,30 @@ __global__ void __launch_bounds__(kPThreads, 1)
   constexpr int ST = S::kStages, NB = D / 64;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (kv_smem(raw) & 1023u)) & 1023u);
+  // Barriers.  Those of a query tile, then those of the ring, then the items'.
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + S::kBars);
-  uint64_t *s_full = q_full + 2, *p_full = q_full + 4, *o_done = q_full + 6, *p_half = q_full + 8, *s_free = q_full + 10, *fix = q_full + 12;
-  uint64_t *k_full = q_full + 13, *k_empty = k_full + ST, *v_full = k_empty + ST, *v_empty = v_full + ST;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(v_empty + ST);
-  int* found = reinterpret_cast<int*>(tmem_at + 1);  // sequence's first row, rows, block
-  volatile int* abort = found + 3;
-  int* wsum = found + 4;
+  uint64_t *q_empty = q_full + 2, *s_full = q_full + 4, *s_free = q_full + 6, *p_half = q_full + 8, *p_full = q_full + 10,
+           *o_done = q_full + 12, *o_free = q_full + 14, *fix = q_full + 16;
+  uint64_t *k_full = q_full + 17, *k_empty = k_full + ST, *v_full = k_empty + ST, *v_empty = v_full + ST;
+  uint64_t *item_full = v_empty + ST, *item_empty = item_full + 2;
+  PromptItem* items = reinterpret_cast<PromptItem*>(item_empty + 2);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(items + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_at + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  // Which sequence and block: blocks are numbered along the sequences, the last first (the
-  // longest rows of a sequence start first), heads of a block side by side.
-  const int head = blockIdx.x % a.n_heads, blk = a.n_blocks - 1 - blockIdx.x / a.n_heads;
   if (tid == 0) {
-    found[0] = -1;
     *abort = 0;
     for (int i = 0; i < 2; ++i) {
       bar_init(q_full + i, 1);
+      bar_init(q_empty + i, 1);
       bar_init(s_full + i, 1);
-      bar_init(p_full + i, 4);
-      bar_init(p_half + i, 4);
       bar_init(s_free + i, 4);
+      bar_init(p_half + i, 4);
+      bar_init(p_full + i, 4);
       bar_init(o_done + i, 1);
+      bar_init(o_free + i, 4);
+      bar_init(item_full + i, 1);
+      bar_init(item_empty + i, 11);  // softmax, TMA and MMA warps
     }
     bar_init(fix, 1);
     for (int i = 0; i < ST; ++i) {
@@ -243,44 +272,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  int carry = 0;
-  for (int base = 0; base < a.n_seqs; base += kPThreads) {
-    const int b = base + tid;
-    int s = 0, e = 0;
-    if (b < a.n_seqs) {
-      s = a.cu[b];
-      e = a.cu[b + 1];
-      if (s < 0 || e < s || e > a.n_tokens) {
-        kv_flag(a.error, MOE_DEVERR_PAGE);
-        e = s;
-      }
-    }
-    const int mine = (e - s + 2 * kPM - 1) / (2 * kPM);
-    int v = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, off);
-      if (lane >= off) v += y;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = v;
-    __syncthreads();
-    int sum = carry;
-    for (int w = 0; w < kPThreads / 32; ++w) {
-      if (w < warp) sum += wsum[w];
-      carry += wsum[w];
-    }
-    const int first = sum + v - mine;
-    if (blk >= first && blk < first + mine) {
-      found[0] = s;
-      found[1] = e - s;
-      found[2] = blk - first;
-    }
-  }
-  __syncthreads();
-  const int row0 = found[0], n = found[1], qb = found[2];
-  if (row0 < 0) return;  // the grid is an upper bound
-
+  int seq_row = 0, seq_rows = 0, seq_blocks = 0;  // of this lane's sequence (warp 11), read while the rest is set up
+  if (warp == 11) seq_blocks = prompt_blocks(a, lane, &seq_row, &seq_rows);
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(kv_smem(tmem_at)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -289,11 +282,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *tmem_at;
-  // key tiles of the two query tiles
-  const int kv_tiles = (n + kPN - 1) / kPN;
-  const int n0 = 2 * qb + 1, n1 = 2 * qb + 2 <= kv_tiles ? 2 * qb + 2 : 0;
-  const int n_kv = n1 ? n1 : n0;
   const uint32_t qa = kv_smem(sm + S::kQ), ka = kv_smem(sm + S::kK), va = kv_smem(sm + S::kV);
+
+  // The next item of a role, or one without rows when there are no more (or a wait ran out).
+  auto take = [&](int turn) {
+    PromptItem it{-1, 0, 0, 0};
+    if (__all_sync(0xffffffffu, bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort))) {
+      it = items[turn & 1];
+      __syncwarp();
+      if (lane == 0) bar_arrive(item_empty + (turn & 1));
+    }
+    return it;
+  };
 
   // Registers: the softmax warps hold a row of 128 products each; 2 x 208 + 88 are the
   // 3 x 168 that the kernel was launched with.
@@ -302,14 +302,27 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    const int w = warp >> 2, row = (warp & 3) * 32 + lane;
-    const int nt = w ? n1 : n0;
+    const int w = warp >> 2;
+    auto row = [] { return (int)(threadIdx.x & (kPM - 1)); };  // rarely used: not worth a register
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t st = tmem + lanes + M::s(w), pt = tmem + lanes + M::p(w), ot = tmem + lanes + M::o(w);
-    float m = -INFINITY, l = 0.0f;  // m in units of S
     bool ok = true;
-    for (int j = 0; j < nt && ok; ++j) {
-      ok = __all_sync(0xffffffffu, bar_wait(s_full + w, j & 1, abort));
+    int done = 0;  // key tiles of the items before: the barriers' phases go on
+    for (int turn = 0; ok; ++turn) {
+     // The item stays in its slot until its output is written, so that only its number of key
+     // tiles is in registers meanwhile.
+     if (!__all_sync(0xffffffffu, bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort))) break;
+     const volatile PromptItem* slot = items + (turn & 1);
+     const int nt = slot->row0 < 0 ? -1 : PromptItem{0, slot->n, slot->block, 0}.tiles(w);
+     if (nt <= 0) {
+       __syncwarp();
+       if (lane == 0) bar_arrive(item_empty + (turn & 1));
+       if (nt) break;
+       continue;
+     }
+     float m = -INFINITY, l = 0.0f;  // m in units of S
+     for (int j = 0; j < nt && ok; ++j) {
+      ok = __all_sync(0xffffffffu, bar_wait(s_full + w, (done + j) & 1, abort));
       if (!ok) break;
       tc_after();
       uint32_t s[128];
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) bar_arrive(s_free + w);
       if (j == nt - 1) {  // the diagonal tile: keys behind the row (and so behind the sequence)
 #pragma unroll
-        for (int c = 0; c < 128; ++c) f[c] = c > row ? -INFINITY : f[c];
+        for (int c = 0; c < 128; ++c) f[c] = c > row() ? -INFINITY : f[c];
       }
       float mx[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         m = mn;
         l *= al;
         if (j > 0) {
-          ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (j - 1) & 1, abort));
+          ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + j - 1) & 1, abort));
           if (!ok) break;
           tc_after();
 #pragma unroll 1
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       uint32_t p[16];
       weights(0, p);
       if (j > 0) {  // P of the tile before must have been used
-        ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (j - 1) & 1, abort));
+        ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + j - 1) & 1, abort));
         if (!ok) break;
         tc_after();
       }
@@ -399,71 +412,90 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(p_full + w);
     }
-    if (nt > 0) {
-      if (ok) ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (nt - 1) & 1, abort));
-      tc_after();
-      const int r = qb * 2 * kPM + w * kPM + row;
-      const float inv = ok ? 1.0f / l : __int_as_float(0x7fc00000);
-      if (!ok && lane == 0) kv_flag(a.error, MOE_DEVERR_TMA);
-      T* dst = static_cast<T*>(a.out) + (int64_t)(row0 + r) * a.o_tok + head * a.o_head;
+     if (ok) ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + nt - 1) & 1, abort));
+     done += nt;
+     tc_after();
+     const PromptItem it{slot->row0, slot->n, slot->block, slot->head};
+     __syncwarp();
+     if (lane == 0) bar_arrive(item_empty + (turn & 1));
+     const int r = it.block * 2 * kPM + w * kPM + row();
+     const float inv = ok ? 1.0f / l : __int_as_float(0x7fc00000);
+     if (!ok && lane == 0) kv_flag(a.error, MOE_DEVERR_TMA);
+     T* dst = static_cast<T*>(a.out) + (int64_t)(it.row0 + r) * a.o_tok + it.head * a.o_head;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tm_ld32(ot + c, o);
-        tm_wait_ld();
-        tm_landed32(o);
-        if (r < n) {
-          uint32_t p[16];
+     for (int c = 0; c < D; c += 32) {
+       uint32_t o[32];
+       tm_ld32(ot + c, o);
+       tm_wait_ld();
+       tm_landed32(o);
+       if (c == D - 32) {  // O may be written again
+         tc_before();
+         __syncwarp();
+         if (lane == 0) bar_arrive(o_free + w);
+       }
+       if (r < it.n) {
+         uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-          if (a.vec) {
+         for (int i = 0; i < 16; ++i) p[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+         if (a.vec) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-          } else {
+           for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) reinterpret_cast<uint16_t*>(dst + c)[i] = (uint16_t)(p[i >> 1] >> (16 * (i & 1)));
-          }
-        }
-      }
+           for (int i = 0; i < 32; ++i) reinterpret_cast<uint16_t*>(dst + c)[i] = (uint16_t)(p[i >> 1] >> (16 * (i & 1)));
+         }
+       }
+     }
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- TMA
-    const int kh = head / a.group;
-    if (lane == 0) {
-      for (int w = 0; w < (n1 ? 2 : 1); ++w) {
-        bar_expect(q_full + w, S::kTileB);
-        for (int c = 0; c < NB; ++c)
-          tma3(qa + w * S::kTileB + c * S::kBox, &mq, 64 * c, head, row0 + qb * 2 * kPM + w * kPM, q_full + w);
-      }
-    }
-    for (int j = 0; j < n_kv; ++j) {
-      const int s = j % ST, it = j / ST;
-      bool ok = true;
-      if (it) ok = bar_wait(k_empty + s, (it - 1) & 1, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) {
-        bar_expect(k_full + s, S::kTileB);
-        for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, row0 + j * kPN, k_full + s);
-      }
-      if (it) ok = bar_wait(v_empty + s, (it - 1) & 1, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int left = n - j * kPN;  // keys of this tile that are the sequence's
-      uint64_t* vb = left < kPN ? fix : v_full + s;
-      if (lane == 0) {
-        bar_expect(vb, S::kTileB);
-        for (int c = 0; c < NB; ++c) tma3(va + s * S::kTileB + c * S::kBox, &mv, 64 * c, kh, row0 + j * kPN, vb);
-      }
-      if (left < kPN) {
-        // Values behind the sequence (another one's, perhaps not finite) meet weights of 0:
-        // they are cleared before the product sees them.
-        if (!__all_sync(0xffffffffu, bar_wait(fix, 0, abort))) break;
-        for (int i = lane; i < (kPN - left) * NB * 8; i += 32) {
-          const int r = left + i / (NB * 8), c = (i / 8) % NB;
-          *reinterpret_cast<uint4*>(sm + S::kV + s * S::kTileB + c * S::kBox + r * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+    bool ok = true;
+    int kv = 0, fixes = 0, loads[2] = {0, 0};  // key tiles, cleared tails and query tiles so far
+    for (int turn = 0; ok; ++turn) {
+      const PromptItem it = take(turn);
+      if (it.row0 < 0) break;
+      const int kh = it.head / a.group, n_kv = it.tiles(it.tiles(1) ? 1 : 0);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!ok || !it.tiles(w)) continue;
+        if (loads[w]) ok = __all_sync(0xffffffffu, bar_wait(q_empty + w, (loads[w] - 1) & 1, abort));
+        if (ok && lane == 0) {
+          bar_expect(q_full + w, S::kTileB);
+          for (int c = 0; c < NB; ++c)
+            tma3(qa + w * S::kTileB + c * S::kBox, &mq, 64 * c, it.head, it.row0 + it.block * 2 * kPM + w * kPM, q_full + w);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(v_full + s);
+        ++loads[w];
+      }
+      for (int j = 0; j < n_kv && ok; ++j, ++kv) {
+        const int s = kv % ST, round = kv / ST;
+        if (round) ok = __all_sync(0xffffffffu, bar_wait(k_empty + s, (round - 1) & 1, abort));
+        if (!ok) break;
+        if (lane == 0) {
+          bar_expect(k_full + s, S::kTileB);
+          for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, it.row0 + j * kPN, k_full + s);
+        }
+        if (round) ok = __all_sync(0xffffffffu, bar_wait(v_empty + s, (round - 1) & 1, abort));
+        if (!ok) break;
+        const int left = it.n - j * kPN;  // keys of this tile that are the sequence's
+        uint64_t* vb = left < kPN ? fix : v_full + s;
+        if (lane == 0) {
+          bar_expect(vb, S::kTileB);
+          for (int c = 0; c < NB; ++c) tma3(va + s * S::kTileB + c * S::kBox, &mv, 64 * c, kh, it.row0 + j * kPN, vb);
+        }
+        if (left < kPN) {
+          // Values behind the sequence (another one's, perhaps not finite) meet weights of 0:
+          // they are cleared before the product sees them.
+          ok = __all_sync(0xffffffffu, bar_wait(fix, fixes & 1, abort));
+          if (!ok) break;
+          ++fixes;
+          for (int i = lane; i < (kPN - left) * NB * 8; i += 32) {
+            const int r = left + i / (NB * 8), c = (i / 8) % NB;
+            *reinterpret_cast<uint4*>(sm + S::kV + s * S::kTileB + c * S::kBox + r * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) bar_arrive(v_full + s);
+        }
       }
     }
   } else if (warp < 11) {
@@ -477,69 +509,143 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr uint32_t base = (1u << 4) | (ty << 7) | (ty << 10) | ((uint32_t)(kPM >> 4) << 24);
     const bool leader = elect_one();
     bool ok = true;
+    // Phases of the barriers, in the bits of one word (uniform registers are scarce: counters cost
+    // a reload at every product): of the ring, and for query tile w at bits w, w + 2, w + 4.
+    int s = 0;
+    uint32_t ring = 0, bits = 0;
     if (warp == 9) {
-      // S of key tile j, tile 0 then tile 1; the columns are free when the softmax warps have the
-      // tile before that used them in registers: the other query tile's where they share them, else its own.
+      // S of key tile j, tile 0 then tile 1; the columns are free when the softmax warps have what
+      // was in them in registers: the other query tile's S where they share them, else its own.
       constexpr uint32_t id_s = base | ((uint32_t)(kPN >> 3) << 17);
       const uint64_t qd = op_desc(qa, 16), kd = op_desc(ka, 16);
-      for (int j = 0; j < n_kv && ok; ++j) {
-        ok = bar_wait(k_full + j % ST, (j / ST) & 1, abort);
+      int last = -1;  // whose S was issued last
+      for (int turn = 0; ok; ++turn) {
+        const PromptItem it = take(turn);
+        if (it.row0 < 0) break;
+        const int n0 = it.tiles(0), n1 = it.tiles(1), n_kv = n1 ? n1 : n0;
+        for (int j = 0; j < n_kv && ok; ++j) {
+          ok = bar_wait(k_full + s, ring, abort);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (!ok || j >= (w ? n1 : n0)) continue;
-          if (j == 0) ok = bar_wait(q_full + w, 0, abort);
-          if (M::kS == 2 || !n1) {
-            if (j > 0 && ok) ok = bar_wait(s_free + w, (j - 1) & 1, abort);
-          } else if (w == 1) {
-            if (ok) ok = j < n0 ? bar_wait(s_free, j & 1, abort) : bar_wait(s_free + 1, (j - 1) & 1, abort);
-          } else if (j > 0 && ok) {
-            ok = bar_wait(s_free + 1, (j - 1) & 1, abort);
-          }
-          if (!ok) continue;
-          tc_after();
-          if (leader) {
-            const uint64_t q = qd + w * (S::kTileB >> 4), k = kd + (j % ST) * (S::kTileB >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = ((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4;
-              mma_ss(tmem + M::s(w), q + o, k + o, id_s, kk > 0);
+          for (int w = 0; w < 2; ++w) {
+            const int nt = w ? n1 : n0;
+            if (!ok || j >= nt) continue;
+            if (j == 0) {  // bit w: queries read
+              ok = bar_wait(q_full + w, bits >> w & 1, abort);
+              bits ^= 1u << w;
             }
-            commit(s_full + w);
-            if (w == 1 || !n1) commit(k_empty + j % ST);
+            // bit w + 2: the phase of s_free that the last S of tile w completes; bit w + 4: there was one
+            if (M::kS == 2) {
+              if (ok && (bits >> (4 + w) & 1)) ok = bar_wait(s_free + w, bits >> (2 + w) & 1, abort);
+            } else if (ok && last >= 0) {
+              ok = bar_wait(s_free + last, bits >> (2 + last) & 1, abort);
+            }
+            if (!ok) continue;
+            tc_after();
+            if (leader) {
+              const uint64_t q = qd + w * (S::kTileB >> 4), k = kd + s * (S::kTileB >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + M::s(w), q + o, k + o, id_s, kk > 0);
+              }
+              commit(s_full + w);
+              if (w == 1 || !n1) commit(k_empty + s);
+              if (j == nt - 1) commit(q_empty + w);
+            }
+            __syncwarp();
+            if (bits >> (4 + w) & 1) bits ^= 4u << w; else bits |= 16u << w;
+            last = w;
           }
-          __syncwarp();
+          if (++s == ST) s = 0, ring ^= 1;
         }
       }
     } else {
       constexpr uint32_t id_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
       const uint64_t vd = op_desc(va, S::kBox);
-      for (int j = 0; j < n_kv && ok; ++j) {
-        ok = bar_wait(v_full + j % ST, (j / ST) & 1, abort);
+      for (int turn = 0; ok; ++turn) {
+        const PromptItem it = take(turn);
+        if (it.row0 < 0) break;
+        const int n0 = it.tiles(0), n1 = it.tiles(1), n_kv = n1 ? n1 : n0;
+        for (int j = 0; j < n_kv && ok; ++j) {
+          ok = bar_wait(v_full + s, ring, abort);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (j >= (w ? n1 : n0)) continue;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (ok) ok = bar_wait((half ? p_full : p_half) + w, j & 1, abort);
-            if (!ok) continue;
-            tc_after();
-            if (leader) {
-              const uint64_t v = vd + (j % ST) * (S::kTileB >> 4);
-#pragma unroll
-              for (int kk = 0; kk < kPN / 32; ++kk) {
-                const int k = half * (kPN / 32) + kk;
-                mma_ts(tmem + M::o(w), tmem + M::p(w) + k * 8, v + k * (2048 >> 4), id_o, j > 0 || k > 0);
-              }
-              if (half) {
-                commit(o_done + w);
-                if (w == 1 || !n1) commit(v_empty + j % ST);
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || j >= (w ? n1 : n0)) continue;
+            if (j == 0) {  // bit w + 2: the phase of o_free that the last item of tile w completes; bit w + 4: there was one
+              if (bits >> (4 + w) & 1) {
+                ok = bar_wait(o_free + w, bits >> (2 + w) & 1, abort);
+                bits ^= 4u << w;
+              } else {
+                bits |= 16u << w;
               }
             }
-            __syncwarp();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // bit w: weights used
+              if (ok) ok = bar_wait((half ? p_full : p_half) + w, bits >> w & 1, abort);
+              if (!ok) continue;
+              tc_after();
+              if (leader) {
+                const uint64_t v = vd + s * (S::kTileB >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kPN / 32; ++kk) {
+                  const int k = half * (kPN / 32) + kk;
+                  mma_ts(tmem + M::o(w), tmem + M::p(w) + k * 8, v + k * (2048 >> 4), id_o, j > 0 || k > 0);
+                }
+                if (half) {
+                  commit(o_done + w);
+                  if (w == 1 || !n1) commit(v_empty + s);
+                }
+              }
+              __syncwarp();
+            }
+            bits ^= 1u << w;
           }
+          if (++s == ST) s = 0, ring ^= 1;
         }
       }
     }
+  } else {
+    // ---------------------------------------------------------------- items
+    // Longest first: blocks by their number within the sequence (the key tiles they need), the
+    // last ones first; of those with the same number all sequences that have it, of each all
+    // heads side by side (they share keys and values).  Of every gridDim items in that order a
+    // CTA takes one, from the front and from the back in turn (from the front alone, the first
+    // CTA has the longest each time: 925 us against 855 for one prompt of 16384 tokens).
+    int s = seq_row, n = seq_rows, mine = seq_blocks, most = __reduce_max_sync(0xffffffffu, mine);
+    for (int b = 32; b < a.n_seqs; b += 32) {
+      mine = prompt_blocks(a, b + lane, &s, &n);
+      most = max(most, __reduce_max_sync(0xffffffffu, mine));
+    }
+    int turn = 0;
+    int64_t before = 0, want = blockIdx.x;  // items before the sequences looked at; the next one wanted
+    const int64_t step = gridDim.x;
+    bool ok = true;
+    auto give = [&](const PromptItem& it) {
+      if (turn > 1) ok = __all_sync(0xffffffffu, bar_wait(item_empty + (turn & 1), ((turn >> 1) - 1) & 1, abort));
+      if (ok && lane == 0) {
+        items[turn & 1] = it;
+        bar_arrive(item_full + (turn & 1));
+      }
+      ++turn;
+    };
+    const bool few = a.n_seqs <= 32;  // then every lane keeps its sequence
+    for (int q = most - 1; q >= 0 && ok; --q) {
+      for (int b = 0; b < a.n_seqs && ok; b += 32) {
+        if (!few) mine = prompt_blocks(a, b + lane, &s, &n);
+        const uint32_t has = __ballot_sync(0xffffffffu, mine > q);
+        const int64_t here = (int64_t)__popc(has) * a.n_heads;
+        while (want < before + here && ok) {
+          const int k = (int)(want - before) / a.n_heads, head = (int)(want - before) % a.n_heads;
+          // the k-th sequence that has this block
+          const int src = __ffs(__ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == k)) - 1;
+          give(PromptItem{__shfl_sync(0xffffffffu, s, src), __shfl_sync(0xffffffffu, n, src), q, head});
+          const int64_t round = want / step;
+          want = (round + 2) * step - 1 - (want - round * step);
+        }
+        before += here;
+      }
+    }
+    if (ok) give(PromptItem{-1, 0, 0, 0});
   }
   tc_before();
   __syncwarp();
@@ -577,13 +683,17 @@ template <typename T, int D>
 cudaError_t prompt_go(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int device,
                       cudaStream_t st) {
   static bool ready[kKvMaxDevices];
+  const int n_sm = kv_sm_count(device);
+  if (!n_sm) return cudaErrorInvalidDevice;
   if (!ready[device]) {
     const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                PromptSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
     ready[device] = true;
   }
-  attend_prompt_kernel<T, D><<<a.n_blocks * a.n_heads, kPThreads, PromptSmem<D>::kBytes, st>>>(a, mq, mk, mv);
+  const int64_t items = (int64_t)a.n_blocks * a.n_heads;  // at most
+  const int grid = (int)(items < n_sm ? items : n_sm);
+  attend_prompt_kernel<T, D><<<grid, kPThreads, PromptSmem<D>::kBytes, st>>>(a, mq, mk, mv);
   return cudaGetLastError();
 }
 

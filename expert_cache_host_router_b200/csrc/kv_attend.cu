@@ -868,16 +868,6 @@ struct AttendPlan {
   size_t part, ml, ml_whole, pieces, z, total;  // byte offsets
 };
 
-static int sm_count(int dev) {
-  static int n[kKvMaxDevices];
-  if (!n[dev]) {
-    int v = 0;
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    n[dev] = v;
-  }
-  return n[dev];
-}
-
 static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, bool scored, AttendPlan* p) {
   if (n_q_heads < 1 || max_len < 0) return MOE_ERR_INVALID;
   if (n_q_heads % c.heads) return MOE_ERR_INVALID;
@@ -889,7 +879,7 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   const int64_t tiles = p->items * ((max_len + kTileTok - 1) / kTileTok + kItemCost);
   const int per = (max_len + kJoinThreads - 1) / kJoinThreads;
   if (tiles > INT32_MAX / 2 || p->items * 8 * p->nt + (scored ? (int64_t)c.n_seqs * c.heads * per : 0) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  const int sms = sm_count(device);
+  const int sms = kv_sm_count(device);
   if (!sms) return MOE_ERR_CUDA;
   // A run is at least one group a warp, so that short caches are spread no thinner than a
   // CTA's warps.

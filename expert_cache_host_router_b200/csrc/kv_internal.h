@@ -53,6 +53,17 @@ constexpr int kKvMaxSeqs = 8192;
 inline bool kv_dim_ok(int d) { return d == 64 || d == 128; }
 inline int kv_align_ok(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// SMs of a device, 0 if it cannot be asked.
+inline int kv_sm_count(int dev) {
+  static int known[kKvMaxDevices];
+  if (!known[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
 // MOE_OK, or why the description of a pool and its page table cannot be used.
 inline int kv_check(const moe_kv_pool* c, const moe_kv_table* t, KvView* out) {
   if (!c || !t || !c->pool_dev || !t->table_dev) return MOE_ERR_INVALID;
