@@ -682,7 +682,7 @@ bool rows_map(CUtensorMap* m, const moe_rows* r, int tokens, int heads, int dim,
 template <typename T, int D>
 cudaError_t prompt_go(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int device,
                       cudaStream_t st) {
-  static bool ready[kKvMaxDevices];
+  static std::atomic<bool> ready[kKvMaxDevices];
   const int n_sm = kv_sm_count(device);
   if (!n_sm) return cudaErrorInvalidDevice;
   if (!ready[device]) {

@@ -922,7 +922,7 @@ static cudaError_t launch(void (*kernel)(const KvView, const AttendArgs), int gr
 template <typename T, int D, int NT>
 static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendPlan& p, int device, cudaStream_t st) {
   const int smem = AttendSmem<D, NT>::bytes(c.n_seqs);
-  static bool ready[kKvMaxDevices];  // shared-memory limits raised (the same value each time)
+  static std::atomic<bool> ready[kKvMaxDevices];  // shared-memory limits raised (the same value each time)
   if (!ready[device]) {
     static_assert(AttendSmem<D, NT>::kPre + (kKvMaxSeqs + 1) * 4 <= 227 * 1024, "the prefix of the longest batch fits");
     cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);

@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const KvView c, 
   __shared__ int s_digit, s_need;
   const int b = blockIdx.x / c.heads, h = blockIdx.x % c.heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");  // the second kernel starts up meanwhile
   int len = a.lens[b];
   if (len < 0 || len > a.max_len || len > c.width * c.tiles_per_page * kTileTok) {
     if (tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
@@ -547,6 +548,7 @@ __global__ void __launch_bounds__(192) kv_move_kernel(const KvView c, const KvVi
   const int bh = blockIdx.y, b = bh / c.heads, h = bh % c.heads;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x * ROWS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = a.out_lens[b] - r0;  // rows of this CTA, may exceed ROWS
   if (n <= 0) return;
   if (tid < ROWS) {
@@ -701,7 +703,16 @@ extern "C" int moe_kv_evict(const moe_kv_pool* cache, const moe_kv_table* table,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   kv_select_kernel<<<c.n_seqs * c.heads, kSelThreads, 0, st>>>(c, a);
   const dim3 grid((keep + kMoveTiles * kTileTok - 1) / (kMoveTiles * kTileTok), c.n_seqs * c.heads);
-  if (c.dim == 64) kv_move_kernel<64><<<grid, 192, 0, st>>>(c, o, a);
-  else kv_move_kernel<128><<<grid, 192, 0, st>>>(c, o, a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(192);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, c.dim == 64 ? kv_move_kernel<64> : kv_move_kernel<128>, c, o, a) == cudaSuccess ? MOE_OK
+                                                                                                               : MOE_ERR_CUDA;
 }

@@ -17,6 +17,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe_cache.h"
 
 namespace moe {
@@ -53,15 +55,15 @@ constexpr int kKvMaxSeqs = 8192;
 inline bool kv_dim_ok(int d) { return d == 64 || d == 128; }
 inline int kv_align_ok(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// SMs of a device, 0 if it cannot be asked.
+// SMs of a device, 0 if it cannot be asked.  (Calls may come from several threads at once.)
 inline int kv_sm_count(int dev) {
-  static int known[kKvMaxDevices];
-  if (!known[dev]) {
-    int n = 0;
+  static std::atomic<int> known[kKvMaxDevices];
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    known[dev] = n;
+    known[dev].store(n, std::memory_order_relaxed);
   }
-  return known[dev];
+  return n;
 }
 
 // MOE_OK, or why the description of a pool and its page table cannot be used.

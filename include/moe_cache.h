@@ -368,7 +368,12 @@ MOE_API int moe_decode_step_noalloc(const moe_config *cfg, const moe_noalloc_wei
  * them: the kernels do.  A row whose page number, position or length lies outside the
  * described cache is neither read nor written there; error_dev (when not NULL) receives
  * MOE_DEVERR_PAGE if it was 0, and the call's results for that row (moe_kv_load) or that
- * sequence (moe_kv_attend) are NaN. */
+ * sequence and KV head (moe_kv_attend: its outputs and the scores added to) are NaN; a
+ * length that cannot be counts as 0 in moe_kv_evict and leaves scores alone.  A device-side
+ * wait that runs out (2 s) sets MOE_DEVERR_TMA and gives NaN too.
+ *
+ * Limits (else MOE_ERR_UNSUPPORTED): 8192 sequences a call, 1024 KV heads, 1024 query
+ * heads a KV head, 65535 sequences x KV heads in moe_kv_evict, 2^31 positions a sequence. */
 
 /* A cache pool: n_pages pages of page_tokens tokens (a multiple of 16) of every KV head,
  * head_dim 64 or 128, pool_dev 16-byte aligned:
@@ -391,7 +396,8 @@ typedef struct {
 } moe_kv_pool;
 
 /* Page table: page table_dev[b * row_stride + i] holds positions i * page_tokens .. of
- * sequence b; width entries a sequence are valid to read.  At most 8192 sequences. */
+ * sequence b; width entries a sequence are valid to read.  Sequences may share pages that
+ * are only read. */
 typedef struct {
   const int32_t *table_dev;
   int32_t n_seqs, width;
@@ -414,9 +420,10 @@ typedef struct {
  * in a row: rows cu_dev[b] .. cu_dev[b + 1] - 1 (cu_dev: n_seqs + 1 int32, ascending) go to
  * positions start_dev[b] .. of sequence b (start_dev: n_seqs int32, NULL = all 0).  Rows
  * below cu_dev[0] and from cu_dev[n_seqs] on are padding and not read.  Only the bytes of
- * the rows' own positions change.  Two sequences of one call whose tables name the same
- * page at the same positions leave those positions unspecified.  dtype: MOE_BF16, MOE_F16
- * or MOE_F32. */
+ * the rows' own positions change.  Rows of one call that fall on the same place of the same
+ * page (a page named twice) leave that place unspecified.  For 16-bit rows the stored bytes are
+ * the definition's exactly; for fp32 rows x / d is rounded to fp32 first.  dtype: MOE_BF16, MOE_F16 or
+ * MOE_F32. */
 MOE_API int moe_kv_store(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *cu_dev,
                          const int32_t *start_dev, const moe_rows *k, const moe_rows *v, int32_t n_tokens,
                          int32_t dtype, void *stream);
@@ -429,16 +436,17 @@ MOE_API int moe_kv_load(const moe_kv_pool *cache, const moe_kv_table *table, con
 
 /* Attention of one token per sequence over its cached positions:
  *   z_j = scale * q . k_j,  p = softmax(z) over j < len_dev[b],  out = sum_j p_j v_j,
- * scale > 0, for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  q and out are
- * [n_seqs][n_q_heads][head_dim], dtype MOE_BF16 or MOE_F16, and may not overlap.
- * len_dev: n_seqs int32, 0 <= len <= max_len (an upper
- * bound that the host knows; it sizes the launch); a sequence of length 0 gets zeros.  With
+ * scale > 0, for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  q and
+ * out are [n_seqs][n_q_heads][head_dim], dtype MOE_BF16 or MOE_F16, and may not overlap.
+ * len_dev: n_seqs int32, 0 <= len <= max_len (an upper bound that the host knows; it sizes
+ * the launch and the workspace); a sequence of length 0 gets zeros.  With
  * score, the weights are added to it: score[b][h][j] += sum of p_j over the query heads of
  * KV head h, j < len; entries from len on are not touched.  Softmax statistics and sums
  * are fp32; the cached values are rounded to fp16 (q - 8) * d and the weights to fp16.
  * workspace: 16-byte aligned device memory of at least moe_kv_attend_workspace bytes,
- * contents irrelevant; calls that may overlap need one each.  Results do not depend on
- * the run: no atomics. */
+ * contents irrelevant; calls that may overlap need one each.  The same call gives the same
+ * bits every time (no atomics); where a long sum is split depends on all lengths of the
+ * call, so a sequence's last bits may differ between batches. */
 MOE_API int moe_kv_attend(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *len_dev,
                           int32_t max_len, const moe_rows *q, int32_t n_q_heads, int32_t dtype, float scale,
                           const moe_rows *out, const moe_kv_score *score, void *workspace,
@@ -468,7 +476,8 @@ MOE_API int moe_kv_evict(const moe_kv_pool *cache, const moe_kv_table *table, co
  * q and out are [n_tokens][n_q_heads][head_dim], k and v [n_tokens][n_kv_heads][head_dim]
  * (query head h reads KV head h / (n_q_heads / n_kv_heads)); head_dim 64 or 128, dtype
  * MOE_BF16 or MOE_F16; q, k and v 16-byte aligned with strides that are multiples of 8
- * elements.  out may not overlap q, k or v.  scale > 0.  Rows outside every sequence are left as they were.
+ * elements (else MOE_ERR_UNSUPPORTED).  out may not overlap q, k or v.  scale > 0.  Rows
+ * outside every sequence are left as they were.
  * Products and sums are fp32, the weights are rounded to dtype.  A value row that is not
  * finite makes rows of its own sequence from its tile of 128 positions on NaN, also those
  * before it in that tile; never rows of another sequence.  A sequence whose bounds are not

@@ -374,6 +374,110 @@ def test_streams_and_graphs(moe):
         assert torch.equal(s, score)
 
 
+def test_two_streams_at_once(moe):
+    """Different batches on two streams, interleaved many times without waiting in between."""
+    a, b = (Cache(moe, lens, 2, 128, 64, BF, seed=s) for lens, s in (([900, 33, 4000], 1), ([2500, 7], 2)))
+    qa, qb = rnd(3, 16, 128, dtype=BF, seed=5), rnd(2, 16, 128, dtype=BF, seed=6)
+    ra, rb = moe.kv_attend(a.pool, qa, a.table, a.lens), moe.kv_attend(b.pool, qb, b.table, b.lens)
+    pa = moe.attend_prompt(qa.repeat(100, 1, 1), qa[:, :2].repeat(100, 1, 1), qa[:, 2:4].repeat(100, 1, 1), ints([0, 300]))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        outs.append((moe.kv_attend(a.pool, qa, a.table, a.lens, stream=s1), ra))
+        outs.append((moe.kv_attend(b.pool, qb, b.table, b.lens, stream=s2), rb))
+        with torch.cuda.stream(s2):
+            q3 = qa.repeat(100, 1, 1)
+            outs.append((moe.attend_prompt(q3, q3[:, :2], q3[:, 2:4], ints([0, 300])), pa))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in outs)
+
+
+def test_first_calls_of_a_process_can_be_captured(moe):
+    """Every operator captured before it ever ran in the process, then replayed twice."""
+    import subprocess
+    import sys
+    code = """
+import torch, expert_cache_host_router_b200 as moe
+d = "cuda:0"
+i = lambda v: torch.tensor(v, dtype=torch.int32, device=d)
+pool = moe.kv_pool(8, 16, 2, 64)
+q = torch.randn(40, 4, 64, device=d).half(); k = torch.randn(40, 2, 64, device=d).half(); v = torch.randn(40, 2, 64, device=d).half()
+table, out_table, cu, cu20, lens, score = i([[0, 1, 2]]), i([[3, 4]]), i([0, 40]), i([0, 20]), i([40]), torch.zeros(1, 2, 48, device=d)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    p = moe.attend_prompt(q, k, v, cu)
+    moe.kv_store(pool, k, v, table, cu)
+    o = moe.kv_attend(pool, q[39:], table, lens, 48, score=score)
+    n, kept, s = moe.kv_evict(pool, table, lens, 48, score, 20, 4, out_table)
+    kk, vv = moe.kv_load(pool, out_table, cu20, None, 20, torch.float16)
+score.zero_()
+g.replay(); torch.cuda.synchronize()
+first = [x.clone() for x in (p, o, kept, s)]
+score.zero_()
+g.replay(); torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(first, (p, o, kept, s)))
+assert torch.equal(p, moe.attend_prompt(q, k, v, cu)) and torch.equal(o, moe.kv_attend(pool, q[39:], table, lens, 48))
+assert int(n) == 20 and kept[0, 0, -4:].tolist() == [36, 37, 38, 39]
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_own_workspace(moe):
+    c = Cache(moe, [100, 4000], 2, 64, 32, FP)
+    q = rnd(2, 8, 64, dtype=FP, seed=5)
+    need = moe.kv_attend_workspace(c.pool, c.table, 8, 4000)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    ref = moe.kv_attend(c.pool, q, c.table, c.lens, 4000)
+    assert torch.equal(moe.kv_attend(c.pool, q, c.table, c.lens, 4000, workspace=ws), ref)
+    assert torch.equal(moe.kv_attend(c.pool, q, c.table, c.lens, 4000, workspace=ws), ref)
+    with pytest.raises(moe.MoEError):
+        moe.kv_attend(c.pool, q, c.table, c.lens, 4000, workspace=ws[:need - 256])
+    assert moe.kv_attend_workspace(c.pool, c.table, 8, 4000, True) > need
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1.0, 1e30])
+def test_attend_query_range(moe, scale):
+    """Queries far from 1 in size: scaled to the fp16 range by powers of two inside."""
+    c = Cache(moe, [70], 1, 64, 16, BF)
+    q = rnd(1, 4, 64, dtype=F32, seed=5).mul(scale).to(BF)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, scale=0.2 / scale if scale > 1e-20 else 0.2)
+    o, A, _ = reference(q[0].double(), c.k[0], c.v[0], 0.2 / scale if scale > 1e-20 else 0.2)
+    assert float((out[0].double() - o).abs().max()) <= 2.0 ** -7 * float(A.max())
+
+
+@pytest.mark.parametrize("bad", ["table dtype", "lens count", "q head dim", "q rows", "q dtype", "score small", "score dtype",
+                                 "pool view", "out shape", "lens float", "cu count", "mixed types", "evict same table", "keep 0"])
+def test_binding_refusals_on_the_gpu(moe, bad):
+    c = Cache(moe, [30, 40], 2, 64, 16, FP, more=8)
+    q, k = rnd(2, 4, 64, dtype=FP), rnd(5, 2, 64, dtype=FP)
+    cu, score = ints([0, 2, 5]), torch.zeros(2, 2, 48, device=DEV)
+    call = {
+        "table dtype": lambda: moe.kv_attend(c.pool, q, c.table.long(), c.lens),
+        "lens count": lambda: moe.kv_attend(c.pool, q, c.table, c.lens[:1]),
+        "lens float": lambda: moe.kv_attend(c.pool, q, c.table, c.lens.float()),
+        "q head dim": lambda: moe.kv_attend(c.pool, rnd(2, 4, 128, dtype=FP), c.table, c.lens),
+        "q rows": lambda: moe.kv_attend(c.pool, q[:1], c.table, c.lens),
+        "q dtype": lambda: moe.kv_attend(c.pool, q.float(), c.table, c.lens),
+        "score small": lambda: moe.kv_attend(c.pool, q, c.table, c.lens, 48, score=score[..., :40]),
+        "score dtype": lambda: moe.kv_attend(c.pool, q, c.table, c.lens, 48, score=score.double()),
+        "pool view": lambda: moe.kv_attend(c.pool[:, :1], q, c.table, c.lens),
+        "out shape": lambda: moe.kv_attend(c.pool, q, c.table, c.lens, out=q[:, :2]),
+        "cu count": lambda: moe.kv_store(c.pool, k, k, c.table, cu[:2]),
+        "mixed types": lambda: moe.kv_store(c.pool, k, k.float(), c.table, cu),
+        "evict same table": lambda: moe.kv_evict(c.pool, c.table, c.lens, 48, score, 16, 4, c.table),
+        "keep 0": lambda: moe.kv_evict(c.pool, c.table, c.lens, 48, score, 0, 0, ints([[6], [7]])),
+    }[bad]
+    with pytest.raises(moe.MoEError) as e:
+        call()
+    assert e.value.status == moe.MOE_ERR_INVALID
+
+
 # ------------------------------------------------------------------ evict
 
 
