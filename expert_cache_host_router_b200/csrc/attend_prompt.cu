@@ -135,6 +135,38 @@ __device__ __forceinline__ void tm_landed32(uint32_t* r) { asm volatile("" : O32
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// The other CTA of a pair: an address of this CTA's shared memory there, stores, arrivals.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(kv_smem(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool peer_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(kv_smem(b)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool peer_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+  for (int i = 0; i < (1 << 21); ++i) {
+    if (peer_try(b, parity)) return true;
+    if ((i & 1023) == 1023 && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -192,6 +224,11 @@ struct PromptItem {
     const int t = 2 * block + 1 + w;
     return w && t > (n + kPN - 1) / kPN ? 0 : t;
   }
+  // those of CTA r of CL
+  template <int CL>
+  __device__ __forceinline__ int share(int w, int r) const {
+    return CL == 1 ? tiles(w) : (tiles(w) - r + CL - 1) / CL;
+  }
 };
 
 // Blocks of 256 rows of sequence b, its first row and its rows; none if its bounds cannot be.
@@ -214,7 +251,7 @@ struct PromptSmem {
   static constexpr uint32_t kBox = 128 * 128;             // 128 rows of 64 elements
   static constexpr uint32_t kTileB = (D / 64) * kBox;     // a Q, K or V tile
   static constexpr uint32_t kQ = 0, kK = 2 * kTileB, kV = kK + kStages * kTileB, kEnd = kV + kStages * kTileB;
-  static constexpr uint32_t kBars = kEnd, kBytes = kEnd + 512 + 1024;  // + alignment to 1024
+  static constexpr uint32_t kBars = kEnd, kML = kEnd + 512, kBytes = kML + 2048 + 1024;  // + alignment to 1024
 };
 
 // Tensor memory columns.  P has columns of its own, so that S is free as soon as the softmax warps have it in
@@ -229,7 +266,11 @@ struct PromptTmem {
 };
 static_assert(PromptTmem<64>::kS * 128 + 128 + 2 * 64 <= 512 && PromptTmem<128>::kS * 128 + 128 + 2 * 128 <= 512, "512 columns");
 
-template <typename T, int D>
+// CL = 2: a pair of CTAs (a cluster) shares an item.  CTA r takes key tiles r, r + 2, ..; at the end each
+// gives the other its half of the channels of O with the rows' maxima and sums, through
+// distributed shared memory (where Q was), and writes the joined other half.  For calls with fewer
+// items than SMs, where the longest item alone is the call's time.
+template <typename T, int D, int CL>
 __global__ void __launch_bounds__(kPThreads, 1)
     attend_prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv) {
@@ -244,10 +285,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
            *o_done = q_full + 12, *o_free = q_full + 14, *fix = q_full + 16;
   uint64_t *k_full = q_full + 17, *k_empty = k_full + ST, *v_full = k_empty + ST, *v_empty = v_full + ST;
   uint64_t *item_full = v_empty + ST, *item_empty = item_full + 2;
-  PromptItem* items = reinterpret_cast<PromptItem*>(item_empty + 2);
+  // pairs: S of an item done here; Q's place free at the other CTA; its halves arrived; ours read
+  uint64_t *s_all = item_empty + 2, *peer_ready = s_all + 1, *merge_full = s_all + 2, *merged = s_all + 4;
+  PromptItem* items = reinterpret_cast<PromptItem*>(s_all + 5);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_at + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t rank = CL == 1 ? 0 : blockIdx.x % CL;  // in the pair: clusters are consecutive CTAs
 
   if (tid == 0) {
     *abort = 0;
@@ -264,6 +308,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       bar_init(item_empty + i, 11);  // softmax, TMA and MMA warps
     }
     bar_init(fix, 1);
+    bar_init(s_all, 1);
+    bar_init(peer_ready, 1);
+    bar_init(merge_full, 4);
+    bar_init(merge_full + 1, 4);
+    bar_init(merged, 8);
     for (int i = 0; i < ST; ++i) {
       bar_init(k_full + i, 1);
       bar_init(k_empty + i, 1);
@@ -280,6 +329,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   tc_before();
   __syncthreads();
+  if (CL > 1) cluster_sync();  // the other CTA's barriers are there
   tc_after();
   const uint32_t tmem = *tmem_at;
   const uint32_t qa = kv_smem(sm + S::kQ), ka = kv_smem(sm + S::kK), va = kv_smem(sm + S::kV);
@@ -308,18 +358,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t st = tmem + lanes + M::s(w), pt = tmem + lanes + M::p(w), ot = tmem + lanes + M::o(w);
     bool ok = true;
     int done = 0;  // key tiles of the items before: the barriers' phases go on
+    int merges = 0;
     for (int turn = 0; ok; ++turn) {
      // The item stays in its slot until its output is written, so that only its number of key
      // tiles is in registers meanwhile.
      if (!__all_sync(0xffffffffu, bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort))) break;
      const volatile PromptItem* slot = items + (turn & 1);
-     const int nt = slot->row0 < 0 ? -1 : PromptItem{0, slot->n, slot->block, 0}.tiles(w);
-     if (nt <= 0) {
+     const int all = slot->row0 < 0 ? -1 : PromptItem{0, slot->n, slot->block, 0}.tiles(w);
+     if (all <= 0) {
        __syncwarp();
        if (lane == 0) bar_arrive(item_empty + (turn & 1));
-       if (nt) break;
+       if (CL > 1 && all == 0) {  // not before the item before is through: the phases count arrivals
+         if (turn) ok = __all_sync(0xffffffffu, bar_wait(merged, (turn - 1) & 1, abort));
+         if (lane == 0) bar_arrive(merged);
+       }
+       if (all) break;
        continue;
      }
+     const int nt = CL == 1 ? all : PromptItem{0, slot->n, slot->block, 0}.share<CL>(w, rank);
+     const bool diagonal = CL == 1 || (all - 1) % CL == (int)rank;  // the last key tile is this CTA's
      float m = -INFINITY, l = 0.0f;  // m in units of S
      for (int j = 0; j < nt && ok; ++j) {
       ok = __all_sync(0xffffffffu, bar_wait(s_full + w, (done + j) & 1, abort));
@@ -335,7 +392,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc_before();
       __syncwarp();
       if (lane == 0) bar_arrive(s_free + w);
-      if (j == nt - 1) {  // the diagonal tile: keys behind the row (and so behind the sequence)
+      if (j == nt - 1 && diagonal) {  // the diagonal tile: keys behind the row (and so behind the sequence)
 #pragma unroll
         for (int c = 0; c < 128; ++c) f[c] = c > row() ? -INFINITY : f[c];
       }
@@ -412,26 +469,68 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(p_full + w);
     }
-     if (ok) ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + nt - 1) & 1, abort));
+     if (ok && nt) ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + nt - 1) & 1, abort));
      done += nt;
      tc_after();
      const PromptItem it{slot->row0, slot->n, slot->block, slot->head};
      __syncwarp();
      if (lane == 0) bar_arrive(item_empty + (turn & 1));
      const int r = it.block * 2 * kPM + w * kPM + row();
+     constexpr int COLS = D / CL;  // channels that this CTA writes
+     float f0 = 1.0f, f1 = 0.0f;   // weights of its own partial output and of the other's
+     const float* theirs = reinterpret_cast<const float*>(sm + S::kQ) + w * COLS * kPM + row();
+     if constexpr (CL > 1) {
+       const uint32_t other = rank ^ 1;
+       if (ok) ok = __all_sync(0xffffffffu, peer_wait(peer_ready, turn & 1, abort));
+       if (ok) {
+         const uint32_t to = peer_addr(theirs, other);
+#pragma unroll 1
+         for (int c = 0; c < COLS; c += 32) {
+           uint32_t o[32];
+           if (nt) {
+             tm_ld32(ot + other * COLS + c, o);
+             tm_wait_ld();
+             tm_landed32(o);
+           }
+#pragma unroll
+           for (int i = 0; i < 32; ++i) peer_store(to + (c + i) * (kPM * 4), nt ? __uint_as_float(o[i]) : 0.0f);
+         }
+         float* ml = reinterpret_cast<float*>(sm + S::kML) + w * 2 * kPM + row();
+         peer_store(peer_addr(ml, other), m);
+         peer_store(peer_addr(ml + kPM, other), l);
+         asm volatile("fence.acq_rel.cluster;" ::: "memory");
+         __syncwarp();
+         if (lane == 0) peer_arrive(peer_addr(merge_full + w, other));
+         ok = __all_sync(0xffffffffu, peer_wait(merge_full + w, merges & 1, abort));
+         const float m1 = ml[0], l1 = ml[kPM], top = fmaxf(m, m1);
+         f0 = m == top ? 1.0f : ex2((m - top) * a.scale2);
+         f1 = m1 == top ? 1.0f : ex2((m1 - top) * a.scale2);
+         l = l * f0 + l1 * f1;
+       }
+       ++merges;
+     }
      const float inv = ok ? 1.0f / l : __int_as_float(0x7fc00000);
      if (!ok && lane == 0) kv_flag(a.error, MOE_DEVERR_TMA);
-     T* dst = static_cast<T*>(a.out) + (int64_t)(it.row0 + r) * a.o_tok + it.head * a.o_head;
+     T* dst = static_cast<T*>(a.out) + (int64_t)(it.row0 + r) * a.o_tok + it.head * a.o_head + rank * COLS;
 #pragma unroll 1
-     for (int c = 0; c < D; c += 32) {
+     for (int c = 0; c < COLS; c += 32) {
        uint32_t o[32];
-       tm_ld32(ot + c, o);
-       tm_wait_ld();
-       tm_landed32(o);
-       if (c == D - 32) {  // O may be written again
-         tc_before();
-         __syncwarp();
-         if (lane == 0) bar_arrive(o_free + w);
+       if (nt) {
+         tm_ld32(ot + rank * COLS + c, o);
+         tm_wait_ld();
+         tm_landed32(o);
+         if (c == COLS - 32) {  // O may be written again
+           tc_before();
+           __syncwarp();
+           if (lane == 0) bar_arrive(o_free + w);
+         }
+       }
+       if constexpr (CL > 1) {
+#pragma unroll
+         for (int i = 0; i < 32; ++i) {
+           const float own = nt ? __uint_as_float(o[i]) * f0 : 0.0f;
+           o[i] = __float_as_uint(fmaf(theirs[(c + i) * kPM], f1, own));
+         }
        }
        if (r < it.n) {
          uint32_t p[16];
@@ -446,6 +545,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
          }
        }
      }
+     if (CL > 1) {  // Q's place may be loaded again
+       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+       __syncwarp();
+       if (lane == 0) bar_arrive(merged);
+     }
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- TMA
@@ -454,10 +558,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int turn = 0; ok; ++turn) {
       const PromptItem it = take(turn);
       if (it.row0 < 0) break;
-      const int kh = it.head / a.group, n_kv = it.tiles(it.tiles(1) ? 1 : 0);
+      const int kh = it.head / a.group, n_kv = it.share<CL>(it.tiles(1) ? 1 : 0, rank);
+      if (CL > 1 && turn) ok = __all_sync(0xffffffffu, bar_wait(merged, (turn - 1) & 1, abort));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        if (!ok || !it.tiles(w)) continue;
+        if (!ok || !it.share<CL>(w, rank)) continue;
         if (loads[w]) ok = __all_sync(0xffffffffu, bar_wait(q_empty + w, (loads[w] - 1) & 1, abort));
         if (ok && lane == 0) {
           bar_expect(q_full + w, S::kTileB);
@@ -467,20 +572,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ++loads[w];
       }
       for (int j = 0; j < n_kv && ok; ++j, ++kv) {
-        const int s = kv % ST, round = kv / ST;
+        const int s = kv % ST, round = kv / ST, key0 = it.row0 + (j * CL + rank) * kPN;
         if (round) ok = __all_sync(0xffffffffu, bar_wait(k_empty + s, (round - 1) & 1, abort));
         if (!ok) break;
         if (lane == 0) {
           bar_expect(k_full + s, S::kTileB);
-          for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, it.row0 + j * kPN, k_full + s);
+          for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, key0, k_full + s);
         }
         if (round) ok = __all_sync(0xffffffffu, bar_wait(v_empty + s, (round - 1) & 1, abort));
         if (!ok) break;
-        const int left = it.n - j * kPN;  // keys of this tile that are the sequence's
+        const int left = it.n - (j * CL + rank) * kPN;  // keys of this tile that are the sequence's
         uint64_t* vb = left < kPN ? fix : v_full + s;
         if (lane == 0) {
           bar_expect(vb, S::kTileB);
-          for (int c = 0; c < NB; ++c) tma3(va + s * S::kTileB + c * S::kBox, &mv, 64 * c, kh, it.row0 + j * kPN, vb);
+          for (int c = 0; c < NB; ++c) tma3(va + s * S::kTileB + c * S::kBox, &mv, 64 * c, kh, key0, vb);
         }
         if (left < kPN) {
           // Values behind the sequence (another one's, perhaps not finite) meet weights of 0:
@@ -496,6 +601,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           __syncwarp();
           if (lane == 0) bar_arrive(v_full + s);
         }
+      }
+      if (CL > 1) {  // when S is done here, the other CTA may write where Q was
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(s_all, turn & 1, abort));
+        if (ok && lane == 0) peer_arrive(peer_addr(peer_ready, rank ^ 1));
       }
     }
   } else if (warp < 11) {
@@ -522,7 +631,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int turn = 0; ok; ++turn) {
         const PromptItem it = take(turn);
         if (it.row0 < 0) break;
-        const int n0 = it.tiles(0), n1 = it.tiles(1), n_kv = n1 ? n1 : n0;
+        const int n0 = it.share<CL>(0, rank), n1 = it.share<CL>(1, rank), n_kv = n1 ? n1 : n0;
         for (int j = 0; j < n_kv && ok; ++j) {
           ok = bar_wait(k_full + s, ring, abort);
 #pragma unroll
@@ -558,6 +667,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           if (++s == ST) s = 0, ring ^= 1;
         }
+        if (CL > 1) {
+          if (leader && ok) commit(s_all);
+          __syncwarp();
+        }
       }
     } else {
       constexpr uint32_t id_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
@@ -565,7 +678,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int turn = 0; ok; ++turn) {
         const PromptItem it = take(turn);
         if (it.row0 < 0) break;
-        const int n0 = it.tiles(0), n1 = it.tiles(1), n_kv = n1 ? n1 : n0;
+        const int n0 = it.share<CL>(0, rank), n1 = it.share<CL>(1, rank), n_kv = n1 ? n1 : n0;
         for (int j = 0; j < n_kv && ok; ++j) {
           ok = bar_wait(v_full + s, ring, abort);
 #pragma unroll
@@ -617,8 +730,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       most = max(most, __reduce_max_sync(0xffffffffu, mine));
     }
     int turn = 0;
-    int64_t before = 0, want = blockIdx.x;  // items before the sequences looked at; the next one wanted
-    const int64_t step = gridDim.x;
+    int64_t before = 0, want = blockIdx.x / CL;  // items before the sequences looked at; the next one wanted
+    const int64_t step = gridDim.x / CL;
     bool ok = true;
     auto give = [&](const PromptItem& it) {
       if (turn > 1) ok = __all_sync(0xffffffffu, bar_wait(item_empty + (turn & 1), ((turn >> 1) - 1) & 1, abort));
@@ -650,6 +763,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_before();
   __syncwarp();
   __syncthreads();
+  if (CL > 1) cluster_sync();  // neither leaves while the other may still write to it
   if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -679,22 +793,48 @@ bool rows_map(CUtensorMap* m, const moe_rows* r, int tokens, int heads, int dim,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D>
+template <typename T, int D, int CL>
 cudaError_t prompt_go(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int device,
-                      cudaStream_t st) {
+                      int clusters, cudaStream_t st) {
   static std::atomic<bool> ready[kKvMaxDevices];
-  const int n_sm = kv_sm_count(device);
-  if (!n_sm) return cudaErrorInvalidDevice;
   if (!ready[device]) {
-    const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<T, D, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                PromptSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
     ready[device] = true;
   }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(clusters * CL);
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = PromptSmem<D>::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = CL;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attend_prompt_kernel<T, D, CL>, a, mq, mk, mv);
+}
+
+template <typename T>
+cudaError_t prompt_pick(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int dim, int device,
+                        cudaStream_t st) {
+  const int n_sm = kv_sm_count(device);
+  if (!n_sm) return cudaErrorInvalidDevice;
   const int64_t items = (int64_t)a.n_blocks * a.n_heads;  // at most
-  const int grid = (int)(items < n_sm ? items : n_sm);
-  attend_prompt_kernel<T, D><<<grid, kPThreads, PromptSmem<D>::kBytes, st>>>(a, mq, mk, mv);
-  return cudaGetLastError();
+  // Pairs of CTAs where the longest item decides and is long enough to be worth the exchange at
+  // its end.  One prompt of n tokens, us without pairs / with (D = 128): all items on SMs of their
+  // own either way, n = 600 13.7 / 14.2, 1024 20.3 / 17.8, 2048 33.4 / 24.5, 8192 111 / 70; two
+  // items a pair, n = 2048 34.0 / 34.7, 4096 61.7 / 46.9; more items than SMs, 16384 805 / 927.
+  const int64_t each = a.n_tokens / a.n_seqs;
+  const bool pairs = (2 * items <= n_sm && each >= 1024) || (items <= n_sm && each >= 4096);
+  if (pairs) {
+    const int n = (int)(items < n_sm / 2 ? items : n_sm / 2);
+    return dim == 64 ? prompt_go<T, 64, 2>(a, mq, mk, mv, device, n, st) : prompt_go<T, 128, 2>(a, mq, mk, mv, device, n, st);
+  }
+  const int n = (int)(items < n_sm ? items : n_sm);
+  return dim == 64 ? prompt_go<T, 64, 1>(a, mq, mk, mv, device, n, st) : prompt_go<T, 128, 1>(a, mq, mk, mv, device, n, st);
 }
 
 }  // namespace
@@ -742,10 +882,7 @@ extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_ro
   a.vec = kv_align_ok(out->data_dev, 16) && out->token_stride % 8 == 0 && out->head_stride % 8 == 0;
   a.error = error_dev;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (dtype == MOE_BF16)
-    e = head_dim == 64 ? prompt_go<__nv_bfloat16, 64>(a, mq, mk, mv, device, st) : prompt_go<__nv_bfloat16, 128>(a, mq, mk, mv, device, st);
-  else
-    e = head_dim == 64 ? prompt_go<__half, 64>(a, mq, mk, mv, device, st) : prompt_go<__half, 128>(a, mq, mk, mv, device, st);
+  const cudaError_t e = dtype == MOE_BF16 ? prompt_pick<__nv_bfloat16>(a, mq, mk, mv, head_dim, device, st)
+                                          : prompt_pick<__half>(a, mq, mk, mv, head_dim, device, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

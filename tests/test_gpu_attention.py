@@ -599,6 +599,19 @@ def test_prompt_long_and_peaked(moe, dtype):
     check_prompt(out, q, k, v, [0, n], 128 ** -0.5)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim,hq,hkv,lens", [(128, 4, 1, [2100]), (64, 6, 3, [1024]), (64, 7, 7, [5101]), (128, 8, 2, [4096]),
+                                             (128, 2, 1, [100, 2900, 300]), (64, 3, 1, [1500, 900, 700]), (64, 4, 4, [513, 5000, 0, 600])])
+def test_prompt_pairs(moe, dtype, dim, hq, hkv, lens):
+    """Few long items: two CTAs share each (one or several items in turn), odd and even tile counts."""
+    n = sum(lens)
+    q = rnd(n, hq, dim, dtype=dtype, seed=1, std=2.0)
+    k, v = rnd(n, hkv, dim, dtype=dtype, seed=2), rnd(n, hkv, dim, dtype=dtype, seed=3)
+    out = moe.attend_prompt(q, k, v, ints(starts(lens)))
+    check_prompt(out, q, k, v, starts(lens), dim ** -0.5)
+    assert torch.equal(out, moe.attend_prompt(q, k, v, ints(starts(lens))))
+
+
 def test_prompt_packed_views_padding_and_neighbours(moe):
     """q, k, v as views of one fused tensor; rows outside the sequences stay; NaN and infinity in
     a neighbouring sequence and in the padding reach nothing."""
