@@ -58,12 +58,25 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// False after 2^21 attempts of at most about a microsecond each, or soon after another role
-// gave up.  Inline: a call here would make the softmax warps save their row of products.
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tmbarrier.test_wait.parity.shared::cta.b64 q, [%1], %2;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(kv_smem(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// By whole warps.  False after 2^21 attempts of at most about a microsecond each, or soon after
+// another role gave up.  Inline: a call here would make the softmax warps save their row of
+// products.  Most phases are over when they are asked for: a test and a vote then take some 55
+// cycles, an attempt with a time and a loop that each lane leaves by itself 170 (16384 tokens:
+// 817 -> 802 us; 4 heads of 64, 8192 tokens: 72 -> 69).
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, bar_test(b, parity))) return true;
   for (int i = 0; i < (1 << 21); ++i) {
-    if (bar_try(b, parity)) return true;
-    if ((i & 1023) == 1023 && *abort) return false;
+    if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
+    if ((i & 1023) == 1023 && __any_sync(0xffffffffu, *abort)) return false;
   }
   *abort = 1;
   return false;
@@ -158,8 +171,8 @@ __device__ __forceinline__ bool peer_try(uint64_t* b, uint32_t parity) {
 }
 __device__ __forceinline__ bool peer_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
   for (int i = 0; i < (1 << 21); ++i) {
-    if (peer_try(b, parity)) return true;
-    if ((i & 1023) == 1023 && *abort) return false;
+    if (__all_sync(0xffffffffu, peer_try(b, parity))) return true;
+    if ((i & 1023) == 1023 && __any_sync(0xffffffffu, *abort)) return false;
   }
   *abort = 1;
   return false;
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   // The next item of a role, or one without rows when there are no more (or a wait ran out).
   auto take = [&](int turn) {
     PromptItem it{-1, 0, 0, 0};
-    if (__all_sync(0xffffffffu, bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort))) {
+    if (bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort)) {
       it = items[turn & 1];
       __syncwarp();
       if (lane == 0) bar_arrive(item_empty + (turn & 1));
@@ -362,14 +375,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int turn = 0; ok; ++turn) {
      // The item stays in its slot until its output is written, so that only its number of key
      // tiles is in registers meanwhile.
-     if (!__all_sync(0xffffffffu, bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort))) break;
+     if (!bar_wait(item_full + (turn & 1), (turn >> 1) & 1, abort)) break;
      const volatile PromptItem* slot = items + (turn & 1);
      const int all = slot->row0 < 0 ? -1 : PromptItem{0, slot->n, slot->block, 0}.tiles(w);
      if (all <= 0) {
        __syncwarp();
        if (lane == 0) bar_arrive(item_empty + (turn & 1));
        if (CL > 1 && all == 0) {  // not before the item before is through: the phases count arrivals
-         if (turn) ok = __all_sync(0xffffffffu, bar_wait(merged, (turn - 1) & 1, abort));
+         if (turn) ok = bar_wait(merged, (turn - 1) & 1, abort);
          if (lane == 0) bar_arrive(merged);
        }
        if (all) break;
@@ -379,7 +392,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
      const bool diagonal = CL == 1 || (all - 1) % CL == (int)rank;  // the last key tile is this CTA's
      float m = -INFINITY, l = 0.0f;  // m in units of S
      for (int j = 0; j < nt && ok; ++j) {
-      ok = __all_sync(0xffffffffu, bar_wait(s_full + w, (done + j) & 1, abort));
+      ok = bar_wait(s_full + w, (done + j) & 1, abort);
       if (!ok) break;
       tc_after();
       uint32_t s[128];
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         m = mn;
         l *= al;
         if (j > 0) {
-          ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + j - 1) & 1, abort));
+          ok = bar_wait(o_done + w, (done + j - 1) & 1, abort);
           if (!ok) break;
           tc_after();
 #pragma unroll 1
@@ -444,7 +457,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       uint32_t p[16];
       weights(0, p);
       if (j > 0) {  // P of the tile before must have been used
-        ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + j - 1) & 1, abort));
+        ok = bar_wait(o_done + w, (done + j - 1) & 1, abort);
         if (!ok) break;
         tc_after();
       }
@@ -469,7 +482,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(p_full + w);
     }
-     if (ok && nt) ok = __all_sync(0xffffffffu, bar_wait(o_done + w, (done + nt - 1) & 1, abort));
+     if (ok && nt) ok = bar_wait(o_done + w, (done + nt - 1) & 1, abort);
      done += nt;
      tc_after();
      const PromptItem it{slot->row0, slot->n, slot->block, slot->head};
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
      const float* theirs = reinterpret_cast<const float*>(sm + S::kQ) + w * COLS * kPM + row();
      if constexpr (CL > 1) {
        const uint32_t other = rank ^ 1;
-       if (ok) ok = __all_sync(0xffffffffu, peer_wait(peer_ready, turn & 1, abort));
+       if (ok) ok = peer_wait(peer_ready, turn & 1, abort);
        if (ok) {
          const uint32_t to = peer_addr(theirs, other);
 #pragma unroll 1
@@ -501,7 +514,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
          asm volatile("fence.acq_rel.cluster;" ::: "memory");
          __syncwarp();
          if (lane == 0) peer_arrive(peer_addr(merge_full + w, other));
-         ok = __all_sync(0xffffffffu, peer_wait(merge_full + w, merges & 1, abort));
+         ok = peer_wait(merge_full + w, merges & 1, abort);
          const float m1 = ml[0], l1 = ml[kPM], top = fmaxf(m, m1);
          f0 = m == top ? 1.0f : ex2((m - top) * a.scale2);
          f1 = m1 == top ? 1.0f : ex2((m1 - top) * a.scale2);
@@ -559,11 +572,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const PromptItem it = take(turn);
       if (it.row0 < 0) break;
       const int kh = it.head / a.group, n_kv = it.share<CL>(it.tiles(1) ? 1 : 0, rank);
-      if (CL > 1 && turn) ok = __all_sync(0xffffffffu, bar_wait(merged, (turn - 1) & 1, abort));
+      if (CL > 1 && turn) ok = bar_wait(merged, (turn - 1) & 1, abort);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (!ok || !it.share<CL>(w, rank)) continue;
-        if (loads[w]) ok = __all_sync(0xffffffffu, bar_wait(q_empty + w, (loads[w] - 1) & 1, abort));
+        if (loads[w]) ok = bar_wait(q_empty + w, (loads[w] - 1) & 1, abort);
         if (ok && lane == 0) {
           bar_expect(q_full + w, S::kTileB);
           for (int c = 0; c < NB; ++c)
@@ -573,13 +586,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       for (int j = 0; j < n_kv && ok; ++j, ++kv) {
         const int s = kv % ST, round = kv / ST, key0 = it.row0 + (j * CL + rank) * kPN;
-        if (round) ok = __all_sync(0xffffffffu, bar_wait(k_empty + s, (round - 1) & 1, abort));
+        if (round) ok = bar_wait(k_empty + s, (round - 1) & 1, abort);
         if (!ok) break;
         if (lane == 0) {
           bar_expect(k_full + s, S::kTileB);
           for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, key0, k_full + s);
         }
-        if (round) ok = __all_sync(0xffffffffu, bar_wait(v_empty + s, (round - 1) & 1, abort));
+        if (round) ok = bar_wait(v_empty + s, (round - 1) & 1, abort);
         if (!ok) break;
         const int left = it.n - (j * CL + rank) * kPN;  // keys of this tile that are the sequence's
         uint64_t* vb = left < kPN ? fix : v_full + s;
@@ -590,7 +603,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (left < kPN) {
           // Values behind the sequence (another one's, perhaps not finite) meet weights of 0:
           // they are cleared before the product sees them.
-          ok = __all_sync(0xffffffffu, bar_wait(fix, fixes & 1, abort));
+          ok = bar_wait(fix, fixes & 1, abort);
           if (!ok) break;
           ++fixes;
           for (int i = lane; i < (kPN - left) * NB * 8; i += 32) {
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       if (CL > 1) {  // when S is done here, the other CTA may write where Q was
-        if (ok) ok = __all_sync(0xffffffffu, bar_wait(s_all, turn & 1, abort));
+        if (ok) ok = bar_wait(s_all, turn & 1, abort);
         if (ok && lane == 0) peer_arrive(peer_addr(peer_ready, rank ^ 1));
       }
     }
@@ -681,10 +694,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int n0 = it.share<CL>(0, rank), n1 = it.share<CL>(1, rank), n_kv = n1 ? n1 : n0;
         for (int j = 0; j < n_kv && ok; ++j) {
           ok = bar_wait(v_full + s, ring, abort);
+          // The two halves of the weights of each query tile in the order in which they come: with an S each
+          // (D = 64) the tiles keep step, first halves before second ones (9 packed prompts 50.4 -> 48.3 us);
+          // with one S in turn, tile 0 is half a turn ahead.
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
+          for (int i = 0; i < 4; ++i) {
+            const int w = M::kS == 2 ? i & 1 : i >> 1, half = M::kS == 2 ? i >> 1 : i & 1;
             if (!ok || j >= (w ? n1 : n0)) continue;
-            if (j == 0) {  // bit w + 2: the phase of o_free that the last item of tile w completes; bit w + 4: there was one
+            if (j == 0 && half == 0) {  // bit w + 2: the phase of o_free that the last item of tile w completes; bit w + 4: there was one
               if (bits >> (4 + w) & 1) {
                 ok = bar_wait(o_free + w, bits >> (2 + w) & 1, abort);
                 bits ^= 4u << w;
@@ -692,26 +709,24 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 bits |= 16u << w;
               }
             }
+            // bit w: weights used
+            if (ok) ok = bar_wait((half ? p_full : p_half) + w, bits >> w & 1, abort);
+            if (!ok) continue;
+            tc_after();
+            if (leader) {
+              const uint64_t v = vd + s * (S::kTileB >> 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // bit w: weights used
-              if (ok) ok = bar_wait((half ? p_full : p_half) + w, bits >> w & 1, abort);
-              if (!ok) continue;
-              tc_after();
-              if (leader) {
-                const uint64_t v = vd + s * (S::kTileB >> 4);
-#pragma unroll
-                for (int kk = 0; kk < kPN / 32; ++kk) {
-                  const int k = half * (kPN / 32) + kk;
-                  mma_ts(tmem + M::o(w), tmem + M::p(w) + k * 8, v + k * (2048 >> 4), id_o, j > 0 || k > 0);
-                }
-                if (half) {
-                  commit(o_done + w);
-                  if (w == 1 || !n1) commit(v_empty + s);
-                }
+              for (int kk = 0; kk < kPN / 32; ++kk) {
+                const int k = half * (kPN / 32) + kk;
+                mma_ts(tmem + M::o(w), tmem + M::p(w) + k * 8, v + k * (2048 >> 4), id_o, j > 0 || k > 0);
               }
-              __syncwarp();
+              if (half) {
+                commit(o_done + w);
+                if (w == 1 || !n1) commit(v_empty + s);
+              }
             }
-            bits ^= 1u << w;
+            __syncwarp();
+            if (half) bits ^= 1u << w;
           }
           if (++s == ST) s = 0, ring ^= 1;
         }
@@ -723,7 +738,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // last ones first; of those with the same number all sequences that have it, of each all
     // heads side by side (they share keys and values).  Of every gridDim items in that order a
     // CTA takes one, from the front and from the back in turn (from the front alone, the first
-    // CTA has the longest each time: 925 us against 855 for one prompt of 16384 tokens).
+    // CTA has the longest each time: 880 us against 814 for one prompt of 16384 tokens).
     int s = seq_row, n = seq_rows, mine = seq_blocks, most = __reduce_max_sync(0xffffffffu, mine);
     for (int b = 32; b < a.n_seqs; b += 32) {
       mine = prompt_blocks(a, b + lane, &s, &n);
@@ -734,7 +749,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int64_t step = gridDim.x / CL;
     bool ok = true;
     auto give = [&](const PromptItem& it) {
-      if (turn > 1) ok = __all_sync(0xffffffffu, bar_wait(item_empty + (turn & 1), ((turn >> 1) - 1) & 1, abort));
+      if (turn > 1) ok = bar_wait(item_empty + (turn & 1), ((turn >> 1) - 1) & 1, abort);
       if (ok && lane == 0) {
         items[turn & 1] = it;
         bar_arrive(item_full + (turn & 1));
