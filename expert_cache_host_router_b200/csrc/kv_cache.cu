@@ -137,7 +137,7 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 // is at least 2^-13 away from it (both are ratios of 11-bit integers times a power of two), and product
 // and sum are off by less than 2^-20, so adding 2^-18 puts exact borders on their upper side
 // and moves nothing else across: the codes are the definition's, bit for bit.  A division
-// each made the kernel bound by arithmetic (31 us against 16 us for 16383 tokens of 8 heads of 64).
+// each made the kernel bound by arithmetic (31 us against 23 us for 16383 tokens of 8 heads of 64).
 template <typename T>
 __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t lanes, uint32_t* lo_out, uint32_t* hi_out) {
   uint32_t lo = 0, hi = 0;
@@ -650,9 +650,12 @@ static int rows_call(bool store, const moe_kv_pool* cache, const moe_kv_table* t
                   cu, start, n_tokens};
   DeviceScope dev(cache->device);
   if (!dev.ok) return MOE_ERR_CUDA;
-  // Tokens of a CTA: 16 for a prompt (one look-up warp for many rows); 2 for the few of a
-  // decode step, which would otherwise share two or three SMs.
-  const int n_tok = n_tokens >= 2048 ? kMaxTok : 2;
+  // Tokens of a CTA: the fewest, 2 to 16, with which four CTAs an SM take all of them at once.
+  // With more, few tokens share few SMs; with fewer, each CTA's look-ups are paid again.
+  // Storing 4 heads of 128, us with 2 / 4 / 8 / 16 tokens: 32 tokens 6.2 / 7.4 / 9.9 / 14.6,
+  // 2047 12.5 / 9.5 / 10.5 / 13.7, 4096 20.1 / 14.3 / 12.9 / 15.4, 16383 68.8 / 44.8 / 33.2 / 28.9.
+  int n_tok = 2;
+  for (const int sms = kv_sm_count(cache->device); n_tok < kMaxTok && n_tokens > 4 * sms * n_tok;) n_tok *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == MOE_F32) {
     if (vec) rows_launch<float, true>(store, c, a, n_tok, st); else rows_launch<float, false>(store, c, a, n_tok, st);
