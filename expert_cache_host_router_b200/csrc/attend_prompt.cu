@@ -799,9 +799,10 @@ EncodeTiled encode_tiled() {
 }
 
 // Rows [tokens][heads][D] -> boxes of 128 tokens x 64 channels of one head, 128-byte swizzle.
+// (The stride of a single head or row means nothing; the map wants one all the same.)
 bool rows_map(CUtensorMap* m, const moe_rows* r, int tokens, int heads, int dim, int dtype) {
   const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)r->head_stride * 2, (cuuint64_t)r->token_stride * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? r->head_stride : dim) * 2, (cuuint64_t)(tokens > 1 ? r->token_stride : dim) * 2};
   const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
   return encode_tiled()(m, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                         r->data_dev, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -866,13 +867,14 @@ extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_ro
       n_q_heads % n_kv_heads)
     return MOE_ERR_INVALID;
   if ((dtype != MOE_BF16 && dtype != MOE_F16) || !(scale > 0.0f) || scale - scale != 0.0f) return MOE_ERR_INVALID;
-  if (!kv_dim_ok(head_dim) || n_seqs > kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
-  for (const moe_rows* r : {q, k, v}) {  // the TMA's rules
-    if (!kv_align_ok(r->data_dev, 16) || r->token_stride % 8 || r->head_stride % 8) return MOE_ERR_UNSUPPORTED;
-    if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride >= (1ll << 38) || r->head_stride >= (1ll << 38))
+  if (!kv_dim_ok(head_dim) || n_seqs > kKvMaxSeqs || n_tokens > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
+  // The TMA's rules.  It has no documented meaning for a stride of 0.
+  auto stride_ok = [](int64_t s, int n) { return n < 2 || (s > 0 && s < (1ll << 38) && s % 8 == 0); };
+  for (const moe_rows* r : {q, k, v})
+    if (!kv_align_ok(r->data_dev, 16) || !stride_ok(r->token_stride, n_tokens) ||
+        !stride_ok(r->head_stride, r == q ? n_q_heads : n_kv_heads))
       return MOE_ERR_UNSUPPORTED;
-  }
-  if (!kv_align_ok(out->data_dev, 2)) return MOE_ERR_INVALID;
+  if (!kv_align_ok(out->data_dev, 2) || !kv_apart(out->token_stride, n_tokens, out->head_stride, n_q_heads)) return MOE_ERR_INVALID;
   if (n_tokens == 0 || n_seqs == 0) return MOE_OK;
   const int64_t blocks = n_tokens / (2 * kPM) + (n_seqs < n_tokens ? n_seqs : n_tokens);
   if (blocks * n_q_heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;

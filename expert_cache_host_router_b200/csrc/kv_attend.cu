@@ -872,7 +872,7 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   if (n_q_heads < 1 || max_len < 0) return MOE_ERR_INVALID;
   if (n_q_heads % c.heads) return MOE_ERR_INVALID;
   const int group = n_q_heads / c.heads;
-  if (group > 1024) return MOE_ERR_UNSUPPORTED;
+  if (group > 1024 || max_len > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
   // Heads of an item: 16 when there are more than 8, so that a tile is read once for them (us
   // with 8 / 16, 64 sequences of up to 8192, 4 groups of 16 heads of 128: 106 / 94; of 32
   // heads: 197 / 169; one sequence of 700: 9.3 / 10.9); empty columns cost (groups of 8: 60 / 91).
@@ -968,6 +968,8 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   if ((dtype != MOE_BF16 && dtype != MOE_F16) || !(scale > 0.0f) || scale - scale != 0.0f)
     return MOE_ERR_INVALID;
   if (!kv_align_ok(q->data_dev, 2) || !kv_align_ok(out->data_dev, 2)) return MOE_ERR_INVALID;
+  if (!kv_apart(out->token_stride, c.n_seqs, out->head_stride, n_q_heads)) return MOE_ERR_INVALID;
+  if (score && !kv_apart(score->seq_stride, c.n_seqs, score->head_stride, c.heads)) return MOE_ERR_INVALID;
   bad = attend_plan(c, cache->device, n_q_heads, max_len, score != nullptr, &p);
   if (bad) return bad;
   if (c.n_seqs == 0) return MOE_OK;

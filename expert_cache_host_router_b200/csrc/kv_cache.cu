@@ -641,6 +641,10 @@ static int rows_call(bool store, const moe_kv_pool* cache, const moe_kv_table* t
   if (bad) return bad;
   if (!cu || !k || !v || !k->data_dev || !v->data_dev || n_tokens < 0) return MOE_ERR_INVALID;
   if (dtype != MOE_BF16 && dtype != MOE_F16 && dtype != MOE_F32) return MOE_ERR_INVALID;
+  if (n_tokens > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
+  if (!store)
+    for (const moe_rows* r : {k, v})
+      if (!kv_apart(r->token_stride, n_tokens, r->head_stride, c.heads)) return MOE_ERR_INVALID;
   if (n_tokens == 0 || c.n_seqs == 0) return MOE_OK;
   const int es = dtype == MOE_F32 ? 4 : 2;
   if (!kv_align_ok(k->data_dev, es) || !kv_align_ok(v->data_dev, es)) return MOE_ERR_INVALID;
@@ -697,6 +701,7 @@ extern "C" int moe_kv_evict(const moe_kv_pool* cache, const moe_kv_table* table,
   if (max_len < 0 || keep < 1 || recent < 0 || recent > keep || o.n_seqs != c.n_seqs) return MOE_ERR_INVALID;
   if (table->table_dev == out_table->table_dev) return MOE_ERR_INVALID;
   if ((int64_t)o.width * cache->page_tokens < keep) return MOE_ERR_INVALID;
+  if (max_len > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
   if (c.n_seqs == 0) return MOE_OK;
   if ((int64_t)c.n_seqs * c.heads > 65535) return MOE_ERR_UNSUPPORTED;
   const EvictArgs a{len_dev, max_len, score->data_dev, score->seq_stride, score->head_stride,

@@ -51,9 +51,14 @@ struct DeviceScope {
 
 constexpr int kKvMaxDevices = 64;
 constexpr int kKvMaxSeqs = 8192;
+constexpr int kKvMaxPos = INT32_MAX - 4095;  // positions, lengths and rows: roundings up to whole tiles stay in 32 bits
 
 inline bool kv_dim_ok(int d) { return d == 64 || d == 128; }
 inline int kv_align_ok(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Whether n0 x n1 rows with these strides can be written: no two of them on the same place for
+// want of a stride.
+inline bool kv_apart(int64_t s0, int64_t n0, int64_t s1, int64_t n1) { return (n0 < 2 || s0) && (n1 < 2 || s1); }
 
 // SMs of a device, 0 if it cannot be asked.  (Calls may come from several threads at once.)
 inline int kv_sm_count(int dev) {
@@ -73,7 +78,7 @@ inline int kv_check(const moe_kv_pool* c, const moe_kv_table* t, KvView* out) {
   if (c->device < 0 || c->device >= kKvMaxDevices || !kv_align_ok(c->pool_dev, 16)) return MOE_ERR_INVALID;
   if (t->n_seqs < 0 || t->width < 1 || t->row_stride < t->width) return MOE_ERR_INVALID;
   if (!kv_dim_ok(c->head_dim) || c->page_tokens % kTileTok || c->n_kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)t->width * c->page_tokens > INT32_MAX || t->n_seqs > kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)t->width * c->page_tokens > kKvMaxPos || t->n_seqs > kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
   // tiles are numbered in 32 bits: 2^31 of them are 2.4 TB and more
   if ((int64_t)c->n_pages * (c->page_tokens / kTileTok) > INT32_MAX / c->n_kv_heads) return MOE_ERR_UNSUPPORTED;
   *out = {c->pool_dev, c->n_pages, c->n_kv_heads, c->head_dim, c->page_tokens / kTileTok,

@@ -373,7 +373,9 @@ MOE_API int moe_decode_step_noalloc(const moe_config *cfg, const moe_noalloc_wei
  * wait that runs out (2 s) sets MOE_DEVERR_TMA and gives NaN too.
  *
  * Limits (else MOE_ERR_UNSUPPORTED): 8192 sequences a call, 1024 KV heads, 1024 query
- * heads a KV head, 65535 sequences x KV heads in moe_kv_evict, 2^31 positions a sequence. */
+ * heads a KV head, 65535 sequences x KV heads in moe_kv_evict, 2^31 - 4096 positions a sequence,
+ * rows a call and max_len.  A stride of rows or scores that a call writes may not be 0 where
+ * there are two or more (else MOE_ERR_INVALID).  Inference only: nothing is kept for a gradient. */
 
 /* A cache pool: n_pages pages of page_tokens tokens (a multiple of 16) of every KV head,
  * head_dim 64 or 128, pool_dev 16-byte aligned:
@@ -476,7 +478,7 @@ MOE_API int moe_kv_evict(const moe_kv_pool *cache, const moe_kv_table *table, co
  * q and out are [n_tokens][n_q_heads][head_dim], k and v [n_tokens][n_kv_heads][head_dim]
  * (query head h reads KV head h / (n_q_heads / n_kv_heads)); head_dim 64 or 128, dtype
  * MOE_BF16 or MOE_F16; q, k and v 16-byte aligned with strides that are multiples of 8
- * elements (else MOE_ERR_UNSUPPORTED).  out may not overlap q, k or v.  scale > 0.  Rows
+ * elements above 0 (else MOE_ERR_UNSUPPORTED; the stride of a single row or head is not looked at).  out may not overlap q, k or v.  scale > 0.  Rows
  * outside every sequence are left as they were.
  * Products and sums are fp32, the weights are rounded to dtype.  A value row that is not
  * finite makes rows of its own sequence from its tile of 128 positions on NaN, also those

@@ -67,8 +67,12 @@ def test_rows_calls(lib):
             assert f(c, t, *args, None) == INVALID, args
         assert f(None, t, P, P, rows(), rows(), 5, 0, None) == INVALID
         assert f(c, None, P, P, rows(), rows(), 5, 0, None) == INVALID
+        assert f(c, t, P, P, rows(), rows(), 2 ** 31 - 1, 0, None) == UNSUPPORTED
         assert f(c, t, P, None, rows(), rows(), 0, 0, None) == moe.MOE_OK  # nothing to do
         assert f(c, table(n_seqs=0), P, None, rows(), rows(), 5, 0, None) == moe.MOE_OK
+    for bad in (rows(token_stride=0), rows(head_stride=0)):  # rows that are written need places of their own
+        assert lib.moe_kv_load(c, t, P, P, bad, rows(), 5, 0, None) == INVALID
+        assert lib.moe_kv_load(c, t, P, P, rows(), bad, 5, 0, None) == INVALID
 
 
 def test_attend(lib):
@@ -80,9 +84,11 @@ def test_attend(lib):
     for kw in (dict(lens=None), dict(most=-1), dict(hq=0), dict(hq=7), dict(dtype=moe.MOE_F32), dict(dtype=9),
                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")),
                dict(q=rows(data_dev=None)), dict(out=rows(data_dev=None)), dict(q=rows(data_dev=P + 1)),
-               dict(out=rows(data_dev=P + 1)), dict(score=moe.KvScore(None, 8, 8))):
+               dict(out=rows(data_dev=P + 1)), dict(score=moe.KvScore(None, 8, 8)),
+               dict(score=moe.KvScore(P, 0, 100)), dict(score=moe.KvScore(P, 200, 0)), dict(out=rows(token_stride=0)),
+               dict(out=rows(head_stride=0))):
         assert call(**kw) == INVALID, kw
-    assert call(hq=2 * 1025) == UNSUPPORTED
+    assert call(hq=2 * 1025) == UNSUPPORTED and call(most=2 ** 31 - 1) == UNSUPPORTED
     assert lib.moe_kv_attend_workspace(c, t, 8, 100, 0, None) == INVALID
     assert lib.moe_kv_attend_workspace(c, t, 8, -1, 0, ctypes.c_size_t()) == INVALID
     assert lib.moe_kv_attend_workspace(pool(n_kv_heads=1024), table(n_seqs=8192), 1024, 2 ** 30, 0, ctypes.c_size_t()) == UNSUPPORTED
@@ -98,6 +104,7 @@ def test_evict(lib):
                dict(recent=-1), dict(recent=17), dict(out=table(table_dev=P)), dict(out=table(table_dev=2 * P, n_seqs=2)),
                dict(keep=257), dict(out_lens=P), dict(out_lens=None), dict(kept=None), dict(out_score=P)):
         assert call(**kw) == INVALID, kw
+    assert call(most=2 ** 31 - 1) == UNSUPPORTED
 
 
 def test_prompt(lib):
@@ -107,10 +114,11 @@ def test_prompt(lib):
 
     for kw in (dict(dev=-1), dict(dev=64), dict(q=rows(None)), dict(k=rows(None)), dict(v=rows(None)), dict(out=rows(None)),
                dict(cu=None), dict(b=-1), dict(n=-1), dict(hq=0), dict(hkv=0), dict(hq=3), dict(dtype=2), dict(scale=0.0),
-               dict(scale=float("nan")), dict(scale=float("inf")), dict(out=rows(P + 1))):
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(out=rows(P + 1)), dict(out=rows(P, 0, 64)),
+               dict(out=rows(P, 256, 0))):
         assert call(**kw) == INVALID, kw
     for kw in (dict(dim=32), dict(dim=256), dict(b=8193), dict(q=rows(P + 8)), dict(k=rows(P, 12, 64)), dict(v=rows(P, 64, 4)),
-               dict(q=rows(P, -64, 64))):
+               dict(q=rows(P, -64, 64)), dict(k=rows(P, 128, 0)), dict(v=rows(P, 0, 64)), dict(n=2 ** 31 - 1)):
         assert call(**kw) == UNSUPPORTED, kw
     assert call(n=0) == moe.MOE_OK and call(b=0) == moe.MOE_OK
 

@@ -631,6 +631,24 @@ def test_prompt_packed_views_padding_and_neighbours(moe):
     assert bool((out[..., 0] == 9).all()) and bool((out[..., dim + 1] == 9).all())
 
 
+def test_prompt_strides_without_meaning_and_of_zero(moe):
+    """Strides of a single head or row are not looked at; heads that share one row are refused."""
+    n, dim = 200, 64
+    q, k, v = rnd(n, 4, dim, dtype=BF, seed=1), rnd(n, dim, dtype=BF, seed=2), rnd(n, dim, dtype=BF, seed=3)
+    cu = ints([0, n])
+    want = moe.attend_prompt(q, k[:, None], v[:, None], cu)
+    check_prompt(want, q, k[:, None], v[:, None], [0, n], dim ** -0.5)
+    odd = [x.as_strided((n, 1, dim), (dim, 1, 1)) for x in (k, v)]
+    assert torch.equal(want, moe.attend_prompt(q, *odd, cu))
+    row = [x[:1].as_strided((1, 4, dim), (3, dim, 1)) for x in (q, q, q)]
+    assert torch.equal(moe.attend_prompt(*row, ints([0, 1])), q[:1])  # one key: its own value
+    for bad in ((q, k[:, None].expand(n, 4, dim), v[:, None]), (q, k[:, None], v[:1, None].expand(n, 1, dim))):
+        with pytest.raises(moe.MoEError):
+            moe.attend_prompt(*bad, cu)
+    with pytest.raises(moe.MoEError):
+        moe.attend_prompt(q, k[:, None], v[:, None], cu, out=torch.empty_like(q[:, :1]).expand(n, 4, dim))
+
+
 def test_prompt_bad_bounds(moe):
     n = 300
     q = rnd(n, 2, 64, dtype=FP, seed=1)
