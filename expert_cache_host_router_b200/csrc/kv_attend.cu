@@ -40,7 +40,6 @@ struct AttendArgs {
   int max_len, group, n_chunks;  // query heads per KV head; chunks of 8 NT heads that they are split into
   float scale2;                  // scale * log2(e)
   int min_run;                   // tiles a CTA takes at least
-  int join_cols;                 // heads of a joining CTA: 1, or 8 NT
   int vec;                       // rows of q can be read 8 bytes at a time
   float* part;                   // [2 CTAs][8 NT][D] partial outputs, unnormalised
   float* ml;                     // [2 CTAs][8 NT][2] their (m, l)
@@ -714,7 +713,8 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 // The first CTAs join the partial results of items (or write the rows of a sequence without
 // positions: zeros, or NaN when its length cannot be).  With few items (each in many pieces)
 // a CTA takes one head: the pieces' weights are formed once, one thread each, then every thread
-// sums its channel, the pieces in kJoinThreads / D interleaved lines, eight loads in flight.
+// sums four channels, the pieces in interleaved lines, the first eight of a line read before
+// the weights are known.
 // With many items (most of them whole or in two pieces) a CTA takes all heads of an item, so that there are
 // few CTAs to start.  Scored
 // calls then add the weights of keys to the caller's scores, kJoinThreads keys of a sequence
@@ -722,6 +722,7 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 // atomics.
 constexpr int kJoinMax = 1024;  // most pieces of an item: one per CTA of the first kernel
 constexpr int kJoinThreads = 512;
+constexpr int kInFlight = 8;     // pieces that a thread has on their way
 
 // (m, l) of one column of an item over its pieces, by one thread.
 __device__ __forceinline__ void join_ml(const AttendArgs& a, int item, int cols, int col, float* m_out, float* l_out) {
@@ -744,36 +745,38 @@ __device__ __forceinline__ void join_ml(const AttendArgs& a, int item, int cols,
   *l_out = L;
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool HEADS>
 __global__ void __launch_bounds__(kJoinThreads) kv_attend_join(const KvView c, const AttendArgs a) {
-  constexpr int COLS = 8 * NT, WAYS = kJoinThreads / D;
+  constexpr int COLS = 8 * NT, WAYS = kJoinThreads / (D / 4);
   __shared__ float sm_m[kJoinMax], sm_l[kJoinMax];  // pieces of an item; heads of a KV head
-  __shared__ float red[kJoinThreads], red_l[WAYS];
+  __shared__ float4 red[kJoinThreads];
+  __shared__ float red_m[kJoinThreads / 32], red_l[WAYS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = c.heads * a.n_chunks, all = c.n_seqs * items;
-  const int n_join = all * (COLS / a.join_cols);
+  constexpr int PER = HEADS ? COLS : 1;  // joining CTAs of an item
+  const int n_join = all * PER;
   const bool joins = (int)blockIdx.x < n_join;
   const int per = (a.max_len + kJoinThreads - 1) / kJoinThreads;
   const int x = (int)blockIdx.x - n_join;
-  const int idx = joins ? blockIdx.x / (COLS / a.join_cols) : 0;
+  const int idx = joins ? blockIdx.x / PER : 0;
   const int b = joins ? idx / items : x / per / c.heads;
   const int len = attend_len(c, a, b);  // an argument of the call: not written by the first kernel
   // Every CTA waits for the first kernel, also one without work: this grid's end stands for both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (joins) {
-    const int col = a.join_cols == 1 ? blockIdx.x % COLS : 0, item = idx % items;
+    const int col = blockIdx.x % PER, item = idx % items;
     const int h = item / a.n_chunks, chunk = item - h * a.n_chunks;
     const int n_heads = min(COLS, a.group - chunk * COLS);
     if (col >= n_heads) return;
     T* out = static_cast<T*>(a.out) + b * a.o_seq + (int64_t)(h * a.group + chunk * COLS + col) * a.o_head;
     if (len <= 0) {
       if (len < 0 && tid == 0) kv_flag(c.error, MOE_DEVERR_PAGE);
-      const int n = a.join_cols == 1 ? D : n_heads * D;
+      const int n = HEADS ? D : n_heads * D;
       for (int o = tid; o < n; o += kJoinThreads)
         out[(o / D) * a.o_head + o % D] = from_float<T>(len < 0 ? __int_as_float(0x7fc00000) : 0.0f);
       return;
     }
-    if (a.join_cols != 1) {
+    if constexpr (!HEADS) {
       const int2 pc = a.pieces[idx];
       if (pc.y == 1) return;  // one CTA had it whole
       for (int o = tid; o < n_heads * D; o += kJoinThreads) {
@@ -792,44 +795,57 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attend_join(const KvView c, c
         }
         out[hc * a.o_head + ch] = from_float<T>(L != L ? L : O / L);
       }
-      return;
-    }
-    const int2 pc = a.pieces[idx];
-    const int c0 = pc.x, n = pc.y;
-    if (n == 1) return;  // one CTA had it whole
-    float m = -INFINITY;
-    for (int k = tid; k < n; k += kJoinThreads) {
-      const float2 ml = reinterpret_cast<const float2*>(a.ml)[(2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * COLS + col];
-      sm_m[k] = ml.x;
-      sm_l[k] = ml.y;
-      m = fmaxf(m, ml.x);
-    }
+    } else {
+      const int2 pc = a.pieces[idx];
+      const int c0 = pc.x, n = pc.y;
+      if (n == 1) return;  // one CTA had it whole
+      const int ch4 = tid % (D / 4), way = tid / (D / 4);
+      auto piece = [&](int k) { return (2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * COLS + col; };
+      auto fetch = [&](int k0, float4(&v)[kInFlight]) {
 #pragma unroll
-    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
+        for (int i = 0; i < kInFlight; ++i)
+          if (k0 + i * WAYS < n) v[i] = reinterpret_cast<const float4*>(a.part + piece(k0 + i * WAYS) * D)[ch4];
+      };
+      float4 v[kInFlight];
+      fetch(way, v);  // on their way while the weights are formed
+      float m = -INFINITY;
+      for (int k = tid; k < n; k += kJoinThreads) {
+        const float2 ml = reinterpret_cast<const float2*>(a.ml)[piece(k)];
+        sm_m[k] = ml.x;
+        sm_l[k] = ml.y;
+        m = fmaxf(m, ml.x);
+      }
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
-    const int ch = tid % D, way = tid / D;
-    float L = 0.0f, O = 0.0f;
-#pragma unroll 8
-    for (int k = way; k < n; k += WAYS) {
-      const float f = sm_m[k] == m ? 1.0f : exp2_fast(sm_m[k] - m);
-      L = fmaf(sm_l[k], f, L);
-      O = fmaf(a.part[((2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * COLS + col) * D + ch], f, O);
-    }
-    __syncthreads();
-    red[tid] = O;
-    if (ch == 0) red_l[way] = L;
-    __syncthreads();
-    if (way) return;
-    float sum = 0.0f, den = 0.0f;
+      for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (lane == 0) red_m[warp] = m;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WAYS; ++w) {
-      sum += red[w * D + ch];
-      den += red_l[w];
+      for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red_m[w]);
+      float L = 0.0f;
+      float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k0 = way; k0 < n; k0 += kInFlight * WAYS) {
+        if (k0 != way) fetch(k0, v);
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+          const int k = k0 + i * WAYS;
+          if (k >= n) break;
+          const float f = sm_m[k] == m ? 1.0f : exp2_fast(sm_m[k] - m);
+          L = fmaf(sm_l[k], f, L);
+          O = make_float4(fmaf(v[i].x, f, O.x), fmaf(v[i].y, f, O.y), fmaf(v[i].z, f, O.z), fmaf(v[i].w, f, O.w));
+        }
+      }
+      red[tid] = O;
+      if (ch4 == 0) red_l[way] = L;
+      __syncthreads();
+      if (tid >= D) return;
+      float sum = 0.0f, den = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAYS; ++w) {
+        sum += reinterpret_cast<const float*>(red)[w * D + tid];
+        den += red_l[w];
+      }
+      out[tid] = from_float<T>(sum / den);  // a NaN of any piece's sum is in den
     }
-    out[ch] = from_float<T>(sum / den);  // a NaN of any piece's sum is in den
     return;
   }
   const int h = x / per % c.heads;
@@ -937,8 +953,14 @@ static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendP
                           : launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a);
   if (e != cudaSuccess) return e;
   const int per = (a.max_len + kJoinThreads - 1) / kJoinThreads;
-  const int grid = (int)p.items * (8 * NT / a.join_cols) + (a.score ? c.n_seqs * c.heads * per : 0);
-  return launch(kv_attend_join<T, D, NT>, grid, kJoinThreads, 0, st, true, c, a);
+  // Few items have many pieces each: a CTA for every head joins them; of many items each has a
+  // piece or two, and a CTA joins all heads.  Us by head / by item, heads of 128: 4 items of
+  // 131072 positions 32 / 72, 32 items 17.5 / 23, 64 items 18.3 / 20.5, 128 items 29.5 / 28, 1024
+  // items 75 / 52; scored calls 61 / 73, 21.3 / 23.5, 22.9 / 21.7, 35.9 / 31.7, 87 / 64.
+  const bool heads = p.items < 64;
+  const int grid = (int)p.items * (heads ? 8 * NT : 1) + (a.score ? c.n_seqs * c.heads * per : 0);
+  return heads ? launch(kv_attend_join<T, D, NT, true>, grid, kJoinThreads, 0, st, true, c, a)
+               : launch(kv_attend_join<T, D, NT, false>, grid, kJoinThreads, 0, st, true, c, a);
 }
 
 }  // namespace moe
@@ -988,11 +1010,6 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   a.n_chunks = p.chunks;
   a.scale2 = scale * 1.4426950408889634f;
   a.min_run = p.min_run;
-  // Few items have many pieces each: a CTA for every head joins them; of many items each has a
-  // piece or two, and a CTA joins all heads.  Us by head / by item, heads of 128: 4 items of
-  // 131072 positions 32 / 72, 32 items 17.5 / 23, 64 items 18.3 / 20.5, 128 items 29.5 / 28, 1024
-  // items 75 / 52; scored calls 61 / 73, 21.3 / 23.5, 22.9 / 21.7, 35.9 / 31.7, 87 / 64.
-  a.join_cols = p.items < 64 ? 1 : 8 * p.nt;
   a.vec = kv_align_ok(q->data_dev, 8) && q->token_stride % 4 == 0 && q->head_stride % 4 == 0;
   a.part = reinterpret_cast<float*>(ws + p.part);
   a.ml = reinterpret_cast<float*>(ws + p.ml);
