@@ -40,6 +40,7 @@ struct AttendArgs {
   int max_len, group, n_chunks;  // query heads per KV head; chunks of 8 NT heads that they are split into
   float scale2;                  // scale * log2(e)
   int min_run;                   // tiles a CTA takes at least
+  int score_ctas;                // CTAs of a sequence's and KV head's scores
   int vec;                       // rows of q can be read 8 bytes at a time
   float* part;                   // [2 CTAs][8 NT][D] partial outputs, unnormalised
   float* ml;                     // [2 CTAs][8 NT][2] their (m, l)
@@ -716,30 +717,41 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
 // sums four channels, the pieces in interleaved lines, the first eight of a line read before
 // the weights are known.
 // With many items (most of them whole or in two pieces) a CTA takes all heads of an item, so that there are
-// few CTAs to start.  Scored
+// few CTAs to start; it has the pieces of a long one side by side as well (63 sequences of 300
+// positions and one of 65536: 46 us one after the other, 28 so).  Scored
 // calls then add the weights of keys to the caller's scores, kJoinThreads keys of a sequence
-// and KV head a CTA.  A position's weight is summed over its heads in order by one thread: no
+// and KV head at a time.  A position's weight is summed over its heads in order by one thread: no
 // atomics.
 constexpr int kJoinMax = 1024;  // most pieces of an item: one per CTA of the first kernel
 constexpr int kJoinThreads = 512;
 constexpr int kInFlight = 8;     // pieces that a thread has on their way
+constexpr int kItemFlight = 2;   // the same where a CTA joins a whole item: with 4, fewer CTAs fit an SM
+                                 // (64 sequences of up to 8192 44.8 -> 44.4 us, scored calls 19.1 -> 20.8)
 
-// (m, l) of one column of an item over its pieces, by one thread.
+// (m, l) of one column of an item over its pieces, by a warp: right in lane 0.
 __device__ __forceinline__ void join_ml(const AttendArgs& a, int item, int cols, int col, float* m_out, float* l_out) {
+  const int lane = threadIdx.x & 31;
   const int2 pc = a.pieces[item];
+  float M = -INFINITY, L = 0.0f;
+  auto add = [&](float m, float l) {
+    const float mn = fmaxf(M, m);
+    L = L * (M == mn ? 1.0f : exp2_fast(M - mn)) + l * (m == mn ? 1.0f : exp2_fast(m - mn));
+    M = mn;
+  };
   if (pc.y == 1) {
     const float2 ml = reinterpret_cast<const float2*>(a.ml_whole)[(int64_t)item * cols + col];
     *m_out = ml.x;
     *l_out = ml.y;
     return;
   }
-  float M = -INFINITY, L = 0.0f;
-#pragma unroll 4
-  for (int k = 0; k < pc.y; ++k) {
+  for (int k = lane; k < pc.y; k += 32) {
     const float2 ml = reinterpret_cast<const float2*>(a.ml)[(2 * (int64_t)(pc.x + k) + (k == 0 ? 1 : 0)) * cols + col];
-    const float mn = fmaxf(M, ml.x);
-    L = L * (M == mn ? 1.0f : exp2_fast(M - mn)) + ml.y * (ml.x == mn ? 1.0f : exp2_fast(ml.x - mn));
-    M = mn;
+    add(ml.x, ml.y);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    const float m = __shfl_down_sync(0xffffffffu, M, off), l = __shfl_down_sync(0xffffffffu, L, off);
+    add(m, l);
   }
   *m_out = M;
   *l_out = L;
@@ -756,10 +768,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attend_join(const KvView c, c
   constexpr int PER = HEADS ? COLS : 1;  // joining CTAs of an item
   const int n_join = all * PER;
   const bool joins = (int)blockIdx.x < n_join;
-  const int per = (a.max_len + kJoinThreads - 1) / kJoinThreads;
   const int x = (int)blockIdx.x - n_join;
   const int idx = joins ? blockIdx.x / PER : 0;
-  const int b = joins ? idx / items : x / per / c.heads;
+  const int b = joins ? idx / items : x / a.score_ctas / c.heads;
   const int len = attend_len(c, a, b);  // an argument of the call: not written by the first kernel
   // Every CTA waits for the first kernel, also one without work: this grid's end stands for both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -779,21 +790,51 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attend_join(const KvView c, c
     if constexpr (!HEADS) {
       const int2 pc = a.pieces[idx];
       if (pc.y == 1) return;  // one CTA had it whole
-      for (int o = tid; o < n_heads * D; o += kJoinThreads) {
-        const int hc = o / D, ch = o % D;
-        float M = -INFINITY, L = 0.0f, O = 0.0f;
-#pragma unroll 2
-        for (int k = 0; k < pc.y; ++k) {
-          const int64_t at = (2 * (int64_t)(pc.x + k) + (k == 0 ? 1 : 0)) * COLS + hc;
-          const float2 ml = reinterpret_cast<const float2*>(a.ml)[at];
-          const float v = a.part[at * D + ch];
-          const float mn = fmaxf(M, ml.x);
-          const float fo = M == mn ? 1.0f : exp2_fast(M - mn), fk = ml.x == mn ? 1.0f : exp2_fast(ml.x - mn);
-          L = L * fo + ml.y * fk;
-          O = O * fo + v * fk;
-          M = mn;
+      constexpr int LANES = COLS * (D / 4), IW = kJoinThreads / LANES;  // threads of a piece, pieces side by side
+      const int ch4 = tid % (D / 4), hc = tid / (D / 4) % COLS, way = tid / LANES;
+      float M = -INFINITY, L = 0.0f;
+      float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      auto add = [&](float m, float l, const float4& v) {
+        const float mn = fmaxf(M, m);
+        const float fo = M == mn ? 1.0f : exp2_fast(M - mn), fk = m == mn ? 1.0f : exp2_fast(m - mn);
+        L = L * fo + l * fk;
+        O = make_float4(O.x * fo + v.x * fk, O.y * fo + v.y * fk, O.z * fo + v.z * fk, O.w * fo + v.w * fk);
+        M = mn;
+      };
+      if (hc < n_heads) {
+        for (int k0 = way; k0 < pc.y; k0 += kItemFlight * IW) {
+          float2 ml[kItemFlight];
+          float4 v[kItemFlight];
+#pragma unroll
+          for (int i = 0; i < kItemFlight; ++i) {
+            const int k = k0 + i * IW;
+            if (k >= pc.y) break;
+            const int64_t at = (2 * (int64_t)(pc.x + k) + (k == 0 ? 1 : 0)) * COLS + hc;
+            ml[i] = reinterpret_cast<const float2*>(a.ml)[at];
+            v[i] = reinterpret_cast<const float4*>(a.part + at * D)[ch4];
+          }
+#pragma unroll
+          for (int i = 0; i < kItemFlight; ++i) {
+            if (k0 + i * IW >= pc.y) break;
+            add(ml[i].x, ml[i].y, v[i]);
+          }
         }
-        out[hc * a.o_head + ch] = from_float<T>(L != L ? L : O / L);
+      }
+      if (IW > 1) {
+        sm_m[tid] = M;
+        sm_l[tid] = L;
+        red[tid] = O;
+        __syncthreads();
+#pragma unroll
+        for (int w = 1; w < IW; ++w)
+          if (way == 0) add(sm_m[tid + w * LANES], sm_l[tid + w * LANES], red[tid + w * LANES]);
+      }
+      if (way == 0 && hc < n_heads) {
+        T* to = out + hc * a.o_head + 4 * ch4;
+        to[0] = from_float<T>(L != L ? L : O.x / L);
+        to[1] = from_float<T>(L != L ? L : O.y / L);
+        to[2] = from_float<T>(L != L ? L : O.z / L);
+        to[3] = from_float<T>(L != L ? L : O.w / L);
       }
     } else {
       const int2 pc = a.pieces[idx];
@@ -848,38 +889,53 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attend_join(const KvView c, c
     }
     return;
   }
-  const int h = x / per % c.heads;
-  const int key0 = (x % per) * kJoinThreads;
-  if (key0 >= len) return;
-  for (int col = tid; col < a.n_chunks * COLS; col += kJoinThreads) {
+  const int h = x / a.score_ctas % c.heads, step = a.score_ctas * kJoinThreads;
+  int key = x % a.score_ctas * kJoinThreads + tid;
+  if (key - tid >= len) return;
+  const float4* z = reinterpret_cast<const float4*>(a.z + ((int64_t)(b * items + h * a.n_chunks) * a.max_len + key) * COLS);
+  float* score = a.score + b * a.s_seq + h * a.s_head + key;
+  float4 v[COLS / 4];
+  auto fetch = [&](int chunk) {
+#pragma unroll
+    for (int i = 0; i < COLS / 4; ++i) v[i] = z[(int64_t)chunk * a.max_len * (COLS / 4) + i];
+  };
+  float old = 0.0f;
+  if (key < len) {  // on their way while the heads' maxima and sums are joined
+    fetch(0);
+    old = *score;
+  }
+  for (int col = warp; col < a.n_chunks * COLS; col += kJoinThreads / 32) {
     float M, L;
     join_ml(a, b * items + h * a.n_chunks + col / COLS, COLS, col % COLS, &M, &L);
-    sm_m[col] = M;
-    sm_l[col] = 1.0f / L;
+    if (lane == 0) {
+      sm_m[col] = M;
+      sm_l[col] = 1.0f / L;
+    }
   }
   __syncthreads();
-  const int key = key0 + tid;
-  if (key >= len) return;
-  float w = 0.0f;
-  const float* z = a.z + ((int64_t)(b * items + h * a.n_chunks) * a.max_len + key) * COLS;
-  float* score = a.score + b * a.s_seq + h * a.s_head + key;
-  const float old = *score;
-  for (int chunk = 0; chunk < a.n_chunks; ++chunk, z += (int64_t)a.max_len * COLS) {
-    const int n = min(COLS, a.group - chunk * COLS);
-    float4 v[COLS / 4];
+  while (key < len) {
+    float w = 0.0f;
+    for (int chunk = 0; chunk < a.n_chunks; ++chunk) {
+      const int n = min(COLS, a.group - chunk * COLS);
+      if (chunk) fetch(chunk);
 #pragma unroll
-    for (int i = 0; i < COLS / 4; ++i) v[i] = reinterpret_cast<const float4*>(z)[i];
-#pragma unroll
-    for (int i = 0; i < COLS; ++i)
-      if (i < n) w += exp2_fast(reinterpret_cast<const float*>(v)[i] - sm_m[chunk * COLS + i]) * sm_l[chunk * COLS + i];
+      for (int i = 0; i < COLS; ++i)
+        if (i < n) w += exp2_fast(reinterpret_cast<const float*>(v)[i] - sm_m[chunk * COLS + i]) * sm_l[chunk * COLS + i];
+    }
+    *score = old + w;
+    if (len - key <= step) return;
+    key += step;
+    z += (int64_t)step * (COLS / 4);
+    score += step;
+    fetch(0);
+    old = *score;
   }
-  *score = old + w;
 }
 
 // ------------------------------------------------------------------ host
 
 struct AttendPlan {
-  int nt, chunks, n_cta, min_run;
+  int nt, chunks, n_cta, min_run, score_ctas;
   int64_t items;
   size_t part, ml, ml_whole, pieces, z, total;  // byte offsets
 };
@@ -896,13 +952,19 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   p->chunks = (group + 8 * p->nt - 1) / (8 * p->nt);
   p->items = (int64_t)c.n_seqs * c.heads * p->chunks;
   const int64_t tiles = p->items * ((max_len + kTileTok - 1) / kTileTok + kItemCost);
-  const int per = (max_len + kJoinThreads - 1) / kJoinThreads;
-  if (tiles > INT32_MAX / 2 || p->items * 8 * p->nt + (scored ? (int64_t)c.n_seqs * c.heads * per : 0) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const int sms = kv_sm_count(device);
   if (!sms) return MOE_ERR_CUDA;
   // A run is at least one group a warp, so that short caches are spread no thinner than a
   // CTA's warps.
   p->min_run = kAW * kGT;
+  // CTAs for the weights of a sequence's and KV head's keys: one for every 512 that there may be, but no more
+  // than 16 an SM in all, which take blocks in turn: sequences are often far shorter than
+  // max_len, and each CTA without work costs 2 to 3 ns (63 sequences of 300 positions and one of
+  // 65536, 4 KV heads: 111 us with all of them, 39 so; 64 of up to 4096, where all have work: 58 either way).
+  const int64_t per = (max_len + kJoinThreads - 1) / kJoinThreads, rows = (int64_t)c.n_seqs * c.heads;
+  p->score_ctas = (int)(rows * per <= 16 * sms ? per : rows < 16 * sms ? 16 * sms / rows : 1);
+  if (p->items * 8 * p->nt + (scored ? rows * p->score_ctas : 0) > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
   const int64_t most = (tiles + p->min_run - 1) / p->min_run;
   int fill = (p->nt == 1 ? 2 : 1) * sms;
   if (fill > kJoinMax) fill = kJoinMax;
@@ -952,13 +1014,12 @@ static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendP
   cudaError_t e = a.score ? launch(kv_attend_kernel<T, D, NT, true>, p.n_cta, kAW * 32, smem, st, false, c, a)
                           : launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a);
   if (e != cudaSuccess) return e;
-  const int per = (a.max_len + kJoinThreads - 1) / kJoinThreads;
   // Few items have many pieces each: a CTA for every head joins them; of many items each has a
-  // piece or two, and a CTA joins all heads.  Us by head / by item, heads of 128: 4 items of
-  // 131072 positions 32 / 72, 32 items 17.5 / 23, 64 items 18.3 / 20.5, 128 items 29.5 / 28, 1024
-  // items 75 / 52; scored calls 61 / 73, 21.3 / 23.5, 22.9 / 21.7, 35.9 / 31.7, 87 / 64.
-  const bool heads = p.items < 64;
-  const int grid = (int)p.items * (heads ? 8 * NT : 1) + (a.score ? c.n_seqs * c.heads * per : 0);
+  // piece or two, and a CTA joins all heads.  Us by head / by item, heads of 128: 4 items
+  // of 131072 positions 26 / 39, 32 of 8192 16.1 / 17.4, 64 of 4096 19.2 / 17.9, 128 31 / 25, 1024 of 1000
+  // 80 / 51; scored calls 38 / 40, 21.3 / 18.4, 24.7 / 20.4, 41 / 32, 98 / 65.
+  const bool heads = p.items < 32;  // (scores or not: the same bits)
+  const int grid = (int)p.items * (heads ? 8 * NT : 1) + (a.score ? c.n_seqs * c.heads * p.score_ctas : 0);
   return heads ? launch(kv_attend_join<T, D, NT, true>, grid, kJoinThreads, 0, st, true, c, a)
                : launch(kv_attend_join<T, D, NT, false>, grid, kJoinThreads, 0, st, true, c, a);
 }
@@ -1010,6 +1071,7 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   a.n_chunks = p.chunks;
   a.scale2 = scale * 1.4426950408889634f;
   a.min_run = p.min_run;
+  a.score_ctas = p.score_ctas;
   a.vec = kv_align_ok(q->data_dev, 8) && q->token_stride % 4 == 0 && q->head_stride % 4 == 0;
   a.part = reinterpret_cast<float*>(ws + p.part);
   a.ml = reinterpret_cast<float*>(ws + p.ml);

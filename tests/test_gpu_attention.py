@@ -280,6 +280,21 @@ def test_attend_many_short_sequences(moe):
     assert bool(out.isfinite().all())
 
 
+@pytest.mark.parametrize("dim,heads,group", [(64, 2, 4), (128, 1, 40), (64, 3, 12)])
+def test_attend_one_long_sequence_among_short_ones(moe, dim, heads, group):
+    """Items of one piece and of very many in one call; scores of far fewer keys than max_len allows."""
+    lens = [(5 * i) % 40 for i in range(47)] + [30000] + [17] * 16
+    c = Cache(moe, lens, heads, dim, 64, BF)
+    q = rnd(len(lens), heads * group, dim, dtype=BF, seed=5, std=2.0)
+    s0 = torch.rand(len(lens), heads, 30000, device=DEV)
+    score = s0.clone()
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, 30000, score=score)
+    for b in (0, 1, 7, 46, 47, 48, len(lens) - 1):
+        check_attend(out, score.double() - s0.double(), q, c, b, dim ** -0.5)
+        assert torch.equal(score[b, :, lens[b]:], s0[b, :, lens[b]:])
+    assert torch.equal(out, moe.kv_attend(c.pool, q, c.table, c.lens, 30000))
+
+
 def test_attend_strides_and_out(moe):
     c = Cache(moe, [50, 61], 2, 128, 16, BF)
     q = rnd(8, 2, 131, dtype=BF, seed=5)[..., 1:129].transpose(0, 1)  # heads outside, odd offset
