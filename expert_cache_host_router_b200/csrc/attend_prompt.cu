@@ -390,6 +390,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
      }
      const int nt = CL == 1 ? all : PromptItem{0, slot->n, slot->block, 0}.share<CL>(w, rank);
      const bool diagonal = CL == 1 || (all - 1) % CL == (int)rank;  // the last key tile is this CTA's
+     // A tile without keys here waits for no product of this turn, so nothing else keeps it from
+     // being through before the item before is: then `merged` would count its arrivals twice.
+     if (CL > 1 && nt == 0 && turn) ok = bar_wait(merged, (turn - 1) & 1, abort);
      float m = -INFINITY, l = 0.0f;  // m in units of S
      for (int j = 0; j < nt && ok; ++j) {
       ok = bar_wait(s_full + w, (done + j) & 1, abort);
@@ -568,6 +571,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // ---------------------------------------------------------------- TMA
     bool ok = true;
     int kv = 0, fixes = 0, loads[2] = {0, 0};  // key tiles, cleared tails and query tiles so far
+    int products = 0;                          // items with key tiles of this CTA's so far
     for (int turn = 0; ok; ++turn) {
       const PromptItem it = take(turn);
       if (it.row0 < 0) break;
@@ -616,7 +620,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       if (CL > 1) {  // when S is done here, the other CTA may write where Q was
-        if (ok) ok = bar_wait(s_all, turn & 1, abort);
+        // Counted in items that have key tiles here: the other ones (a pair's second CTA has none of a
+        // sequence of up to 128 rows) have no Q either, and their commits could complete with
+        // those of the item before, two phases at once.  With key tiles, the next commit needs keys that
+        // are asked for after this wait.
+        if (ok && n_kv) ok = bar_wait(s_all, products++ & 1, abort);
         if (ok && lane == 0) peer_arrive(peer_addr(peer_ready, rank ^ 1));
       }
     }
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           if (++s == ST) s = 0, ring ^= 1;
         }
-        if (CL > 1) {
+        if (CL > 1 && n_kv) {
           if (leader && ok) commit(s_all);
           __syncwarp();
         }
