@@ -24,6 +24,8 @@
 // 2^-11); weights p are fp16 too.  Queries are scaled by a power of two per head to the fp16
 // range (exact but for channels 2^-24 below the head's largest); cached values are within
 // that range by construction.
+#include <cfloat>
+
 #include "kv_internal.h"
 
 namespace moe {
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
       // 2^-x and 2^x, x the exponent of the largest channel (0 for none, infinity or NaN)
       int x = (int)(__float_as_uint(top) >> 23) - 127;
       if (top == 0.0f || x > 127) x = 0;
-      x = max(min(x, 126), -60);  // smaller queries are 0 to any product
+      x = max(min(x, 126), -126);  // 2^-x in the fp32 range; subnormal bf16 channels still get 8 bits
       const float down = __uint_as_float((uint32_t)(127 - x) << 23);
       float sum = 0.0f;
       uint16_t* frag = reinterpret_cast<uint16_t*>(sm + S::kQuery);
@@ -390,7 +392,10 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
           pt[4 + i] = pt[6 + i] = pt[12 + i] = pt[14 + i] = __half(0);
         }
       }
-      if (lane == 0) reinterpret_cast<float*>(sm + S::kScale)[n * 8 + warp] = a.scale2 * exp2f((float)x);
+      // Kept between the smallest normal number and the largest: m = -inf, or products that are 0, times the
+      // factor must not become NaN, and at these ends no weight depends on the factor's exact value.
+      if (lane == 0)
+        reinterpret_cast<float*>(sm + S::kScale)[n * 8 + warp] = fminf(fmaxf(a.scale2 * exp2f((float)x), FLT_MIN), FLT_MAX);
     }
     __syncthreads();
     uint32_t qf[NT][NB][4], qb[NT][2];

@@ -438,7 +438,8 @@ MOE_API int moe_kv_load(const moe_kv_pool *cache, const moe_kv_table *table, con
 
 /* Attention of one token per sequence over its cached positions:
  *   z_j = scale * q . k_j,  p = softmax(z) over j < len_dev[b],  out = sum_j p_j v_j,
- * scale > 0, for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  q and
+ * scale > 0, for every query head (head h reads KV head h / (n_q_heads / n_kv_heads)).  Queries
+ * of any size are taken, as long as scale * q . k stays in the fp32 range.  q and
  * out are [n_seqs][n_q_heads][head_dim], dtype MOE_BF16 or MOE_F16, and may not overlap.
  * len_dev: n_seqs int32, 0 <= len <= max_len (an upper bound that the host knows; it sizes
  * the launch and the workspace); a sequence of length 0 gets zeros.  With

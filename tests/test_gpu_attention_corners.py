@@ -1,4 +1,4 @@
-"""Corners of the attention operators: packed prompts of which a pair's second CTA has no key tile.
+"""Corners of the attention operators that tests/test_gpu_attention.py passes by.
 
 Against 64 bits, with the tolerances that tests/test_gpu_attention.py derives."""
 import math
@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_attention import BF, DEV, FP, Cache, check_attend, half, ints, moe, quantised, rnd, starts, tables  # noqa: E402,F401
+from test_gpu_attention import BF, DEV, F32, FP, Cache, check_attend, half, ints, moe, quantised, rnd, starts, tables  # noqa: E402,F401
 from test_prompt_items import SHORT_AMONG_LONG, SMS  # noqa: E402
 
 
@@ -47,3 +47,28 @@ def test_prompt_pairs_with_turns_without_key_tiles(moe, dtype, dim, lens, heads)
     for first, m in zip(starts(lens), lens):
         rows = sorted({i for i in [*range(min(m, 130)), *range(m // 2, m // 2 + 5), *range(m - 130, m)] if 0 <= i < m})
         check_rows(out, q, k, v, first, m, rows, dim ** -0.5)
+
+
+# ------------------------------------------------------------------ attend: range of queries and scales
+
+
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("power,scale", [(-80, 1e-30), (-80, 2.0 ** 76), (-80, 1e25), (-120, 2.0 ** 117), (-126, 1e-38), (0, 1e-45),
+                                         (100, 2.0 ** -103), (126, 2.0 ** -126)])
+def test_attend_queries_and_scales_far_from_one(moe, scored, power, scale):
+    """Products of order 1 from tiny queries with a scale that makes up for it; equal weights where
+    both are tiny; bf16 queries down to the subnormal ones."""
+    c = Cache(moe, [70, 1, 600], 2, 64, 16, BF)
+    q = rnd(3, 8, 64, seed=5).clamp(-1.9, 1.9).double().mul(2.0 ** power).to(BF)
+    score = torch.zeros(3, 2, 600, device=DEV)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, 600, scale=scale, score=score if scored else None)
+    for b in range(3):
+        check_attend(out, score.double() if scored else None, q, c, b, scale)
+
+
+def test_attend_zero_queries_and_the_largest_scale(moe):
+    c = Cache(moe, [70, 1], 1, 128, 16, FP)
+    q = torch.zeros(2, 8, 128, dtype=FP, device=DEV)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, scale=3.4e38)
+    for b in range(2):
+        check_attend(out, None, q, c, b, 1.0)
