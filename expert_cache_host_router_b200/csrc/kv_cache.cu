@@ -155,11 +155,19 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t 
     const float m = __uint_as_float((key & 0x7FFFE000u) | key << 31);
     const bool nan = (key & 0x7FFFE000u) > 0x7F800000u;
     d = nan ? __int_as_float(0x7fc00000) : fminf(fmaxf(m * -0.125f, -8188.0f), 8188.0f);
-    const float inv = d == 0.0f ? 0.0f : __frcp_rn(d);
+    float inv = d == 0.0f ? 0.0f : __frcp_rn(d), y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    if (!std::is_same<T, __half>::value && fabsf(inv) > 0x1p100f) {
+      // 1 / d may be beyond fp32 here: both sides 2^64 times as large, which changes no code
+      inv = __frcp_rn(d * 0x1p64f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = x[i] * 0x1p64f;
+    }
     uint32_t q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // round(x / d + 8 + 2^-18) in the low bits of 2^23 + q
-      float r = fminf(fmaf(x[i], inv, 8.0f + 3.814697265625e-6f), 15.0f);
+      float r = fminf(fmaf(y[i], inv, 8.0f + 3.814697265625e-6f), 15.0f);
       if (!std::is_same<T, __half>::value) r = fmaxf(r, 0.0f);  // only a limited d gives less: |x| > 65504
       q[i] = __float_as_uint(r + 8388608.0f);
     }

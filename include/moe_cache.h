@@ -424,7 +424,7 @@ typedef struct {
  * below cu_dev[0] and from cu_dev[n_seqs] on are padding and not read.  Only the bytes of
  * the rows' own positions change.  Rows of one call that fall on the same place of the same
  * page (a page named twice) leave that place unspecified.  For 16-bit rows the stored bytes are
- * the definition's exactly; for fp32 rows x / d is rounded to fp32 first.  dtype: MOE_BF16, MOE_F16 or
+ * the definition's exactly; for fp32 rows d and x / d are rounded to fp32 first.  dtype: MOE_BF16, MOE_F16 or
  * MOE_F32. */
 MOE_API int moe_kv_store(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *cu_dev,
                          const int32_t *start_dev, const moe_rows *k, const moe_rows *v, int32_t n_tokens,

@@ -72,3 +72,40 @@ def test_attend_zero_queries_and_the_largest_scale(moe):
     out = moe.kv_attend(c.pool, q, c.table, c.lens, scale=3.4e38)
     for b in range(2):
         check_attend(out, None, q, c, b, 1.0)
+
+
+# ------------------------------------------------------------------ store: the bytes
+
+
+def codes(pool, table, n, dim):
+    """Codes and scales (keys, values) of the first n positions of one sequence and head 0, from the bytes."""
+    nb = dim // 32
+    raw = pool[table.long()][:, 0].reshape(-1, 18 * dim)
+    kb = raw[:, :8 * dim].reshape(-1, 16, 4, nb, 4).transpose(2, 3).reshape(-1, nb, 16)
+    vb = raw[:, 8 * dim:16 * dim].reshape(-1, 8, 8, nb, 2, 2).permute(0, 1, 4, 3, 2, 5).reshape(-1, nb, 16)
+    kd = raw[:, 16 * dim:17 * dim].contiguous().view(FP).reshape(-1, nb)
+    vd = raw[:, 17 * dim:].contiguous().view(FP).reshape(-1, 8, nb, 2).transpose(2, 3).reshape(-1, nb)
+    return [(torch.cat([b & 15, b >> 4], -1)[:n].double(), d[:n]) for b, d in ((kb, kd), (vb, vd))]
+
+
+@pytest.mark.parametrize("dtype,low,high", [(BF, -133, 127), (FP, -24, 15)])
+def test_store_bytes_are_the_definition(moe, dtype, low, high):
+    """Blocks of every magnitude that the type has, subnormal ones too, with zeros among their channels."""
+    dim, reps = 64, 4
+    power = torch.arange(low, high + 1, device=DEV).repeat_interleave(reps)
+    n = power.numel()
+    x = rnd(n, 2, dim, seed=3).clamp(-1.9, 1.9).double() * 2.0 ** power.double()[:, None, None]
+    x[:, :, ::5] = 0
+    x = x.clamp(-torch.finfo(dtype).max, torch.finfo(dtype).max).to(dtype)
+    k, v = x[:, :1].contiguous(), x[:, 1:].contiguous()
+    table = tables(1, -(-n // 16))
+    pool = moe.kv_pool(table.numel(), 16, 1, dim)
+    moe.kv_store(pool, k, v, table, ints([0, n]))
+    for (q, d), rows in zip(codes(pool, table[0], n, dim), (k, v)):
+        b = rows[:, 0].double().unflatten(-1, (-1, 32))
+        big = b.abs().amax(-1, keepdim=True)
+        m = b.gather(-1, (b.abs() == big).to(torch.int8).argmax(-1, keepdim=True))
+        want_d = (-m / 8).clamp(-8188, 8188)
+        want = torch.where(want_d == 0, torch.full_like(b, 8.0), torch.floor(b / want_d + 8.5)).clamp(0, 15)
+        assert torch.equal(q, want)
+        assert torch.equal(d.view(torch.int16), want_d.squeeze(-1).to(FP).view(torch.int16))
