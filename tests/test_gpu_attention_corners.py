@@ -109,3 +109,28 @@ def test_store_bytes_are_the_definition(moe, dtype, low, high):
         want = torch.where(want_d == 0, torch.full_like(b, 8.0), torch.floor(b / want_d + 8.5)).clamp(0, 15)
         assert torch.equal(q, want)
         assert torch.equal(d.view(torch.int16), want_d.squeeze(-1).to(FP).view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_store_special_values(moe, dtype):
+    """Ties of magnitude (the first value decides), NaN (its whole block), infinities of both signs, zeros."""
+    x = torch.zeros(5, 1, 64, dtype=dtype, device=DEV)
+    x[0, 0, :32] = torch.linspace(-3, 3, 32).to(dtype)
+    x[0, 0, 32:] = torch.linspace(3, -3, 32).to(dtype)
+    x[1, 0, 3] = float("nan")
+    x[2, 0, 7], x[2, 0, 8], x[2, 0, 9] = float("inf"), -float("inf"), 100.0
+    x[3, 0, 7], x[3, 0, 8], x[3, 0, 9] = -float("inf"), float("inf"), -torch.finfo(FP).max
+    x[4, 0, 40] = float("-nan")
+    x[4, 0, 41] = float("inf")
+    table, cu = tables(1, 1), ints([0, 5])
+    pool = moe.kv_pool(1, 16, 1, 64)
+    moe.kv_store(pool, x, x, table, cu)
+    for got in moe.kv_load(pool, table, cu, None, 5, F32):
+        got = got[:, 0]
+        assert torch.equal(got[0].double(), quantised(x[0, 0]))
+        assert got[0, 0] == -got[0, 32] and abs(float(got[0, 0])) == 3.0  # the deciding value is kept
+        assert bool(got[1, :32].isnan().all()) and torch.equal(got[1, 32:], torch.zeros(32, device=DEV))
+        assert float(got[2, 7]) == 65504.0 and float(got[2, 8]) == -7 * 8188.0 and float(got[2, 9]) == 0.0
+        assert float(got[3, 7]) == -65504.0 and float(got[3, 8]) == 7 * 8188.0 and float(got[3, 9]) == -65504.0
+        assert bool((got[2, 10:] == 0).all()) and bool((got[3, 10:] == 0).all())
+        assert bool(got[4, 32:].isnan().all()) and bool((got[4, :32] == 0).all())
