@@ -708,6 +708,7 @@ extern "C" int moe_kv_evict(const moe_kv_pool* cache, const moe_kv_table* table,
   if (out_len_dev == len_dev || out_score_dev == score->data_dev) return MOE_ERR_INVALID;
   if (max_len < 0 || keep < 1 || recent < 0 || recent > keep || o.n_seqs != c.n_seqs) return MOE_ERR_INVALID;
   if (table->table_dev == out_table->table_dev) return MOE_ERR_INVALID;
+  if (o.n_seqs > 1 && o.table_stride == 0) return MOE_ERR_INVALID;
   if ((int64_t)o.width * cache->page_tokens < keep) return MOE_ERR_INVALID;
   if (max_len > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
   if (c.n_seqs == 0) return MOE_OK;

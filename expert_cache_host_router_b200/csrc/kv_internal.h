@@ -76,7 +76,7 @@ inline int kv_check(const moe_kv_pool* c, const moe_kv_table* t, KvView* out) {
   if (!c || !t || !c->pool_dev || !t->table_dev) return MOE_ERR_INVALID;
   if (c->n_pages < 1 || c->n_kv_heads < 1 || c->head_dim < 1 || c->page_tokens < 1) return MOE_ERR_INVALID;
   if (c->device < 0 || c->device >= kKvMaxDevices || !kv_align_ok(c->pool_dev, 16)) return MOE_ERR_INVALID;
-  if (t->n_seqs < 0 || t->width < 1 || t->row_stride < t->width) return MOE_ERR_INVALID;
+  if (t->n_seqs < 0 || t->width < 1 || (t->row_stride < t->width && t->row_stride != 0)) return MOE_ERR_INVALID;
   if (!kv_dim_ok(c->head_dim) || c->page_tokens % kTileTok || c->n_kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)t->width * c->page_tokens > kKvMaxPos || t->n_seqs > kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
   // tiles are numbered in 32 bits: 2^31 of them are 2.4 TB and more

@@ -399,7 +399,9 @@ typedef struct {
 
 /* Page table: page table_dev[b * row_stride + i] holds positions i * page_tokens .. of
  * sequence b; width entries a sequence are valid to read.  Sequences may share pages that
- * are only read. */
+ * are only read; with a row_stride of 0 all of them share one row of the table (several new
+ * tokens of one sequence, say, each as a row of a batch), which out_table of moe_kv_evict may
+ * not.  Other strides are at least width. */
 typedef struct {
   const int32_t *table_dev;
   int32_t n_seqs, width;

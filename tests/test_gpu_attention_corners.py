@@ -134,3 +134,35 @@ def test_store_special_values(moe, dtype):
         assert float(got[3, 7]) == -65504.0 and float(got[3, 8]) == 7 * 8188.0 and float(got[3, 9]) == -65504.0
         assert bool((got[2, 10:] == 0).all()) and bool((got[3, 10:] == 0).all())
         assert bool(got[4, 32:].isnan().all()) and bool((got[4, :32] == 0).all())
+
+
+# ------------------------------------------------------------------ tables
+
+
+def test_sequences_that_share_one_table_row(moe):
+    """Several new tokens of one sequence, each a row of the batch: one table row for all of them."""
+    n, t = 90, 5
+    c = Cache(moe, [n], 2, 64, 16, FP)
+    q = rnd(t, 4, 64, dtype=FP, seed=5)
+    lens = ints([n - t + 1 + i for i in range(t)])
+    shared = c.table.expand(t, -1)
+    assert shared.stride(0) == 0
+    score = torch.zeros(t, 2, n, device=DEV)
+    out = moe.kv_attend(c.pool, q, shared, lens, n, score=score)
+    assert torch.equal(out, moe.kv_attend(c.pool, q, shared.contiguous(), lens, n))
+    c.k, c.v = ([x[0][:int(m)] for m in lens] for x in (c.k, c.v))
+    for b in range(t):
+        check_attend(out, score.double(), q, c, b, 64 ** -0.5)
+    # their rows are written and read through it as well, each at a position of its own
+    k, v = rnd(t, 2, 64, dtype=FP, seed=6), rnd(t, 2, 64, dtype=FP, seed=7)
+    cu = ints(range(t + 1))
+    moe.kv_store(c.pool, k, v, shared, cu, lens - 1)
+    gk, gv = moe.kv_load(c.pool, shared, cu, lens - 1, t, F32)
+    assert torch.equal(gk.double(), quantised(k)) and torch.equal(gv.double(), quantised(v))
+    # cut down to different pages each
+    more = moe.kv_pool(c.pool.shape[0] + t, 16, 2, 64)
+    more[:c.pool.shape[0]] = c.pool
+    new, kept, _ = moe.kv_evict(more, shared, lens, n, score, 16, 4, tables(t, 1, first=c.pool.shape[0]))
+    assert new.tolist() == [16] * t and kept[0, 0, -4:].tolist() == [n - t - 3 + i for i in range(4)]
+    with pytest.raises(moe.MoEError):  # but not to the same ones
+        moe.kv_evict(more, shared, lens, n, score, 16, 4, tables(1, 1, first=c.pool.shape[0]).expand(t, -1))
