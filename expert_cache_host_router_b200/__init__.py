@@ -415,7 +415,8 @@ class ExpertCacheMoE:
 # ------------------------------------------------------------------ attention operators
 #
 # torch tensors in, torch tensors out, on the current stream of the tensors' device or on
-# `stream`.  Inference only: no gradient flows through them.  These calls are made once per layer and token, so their arguments are checked
+# `stream`.  Inference only: no gradient flows through them, and rows that require one are refused
+# while gradients are recorded.  These calls are made once per layer and token, so their arguments are checked
 # and converted in an extension module (csrc/bind.cpp) that calls the C ABI.
 
 BIND_PATH = os.path.join(_PKG, "_lib", "_moe_bind.so")

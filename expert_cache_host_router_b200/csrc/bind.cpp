@@ -72,6 +72,14 @@ moe_rows rows_of(const Tensor& t, int64_t n, int64_t heads, int64_t dim, at::Sca
   return {t.data_ptr(), t.stride(0), t.stride(1)};
 }
 
+// These calls keep nothing for a gradient: one that would be lost without a word is refused.
+void no_gradient(std::initializer_list<const Tensor*> rows, const char* what) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor* t : rows)
+    if (t->requires_grad())
+      throw Refused{MOE_ERR_UNSUPPORTED, std::string(what) + ": inference only, but a row tensor requires a gradient (torch.no_grad() or detach())"};
+}
+
 moe_kv_score score_of(const Tensor& t, int64_t n, int64_t heads, int64_t most, c10::Device dev, const char* what) {
   if (t.scalar_type() != at::kFloat || t.dim() != 3 || t.size(0) != n || t.size(1) != heads || t.size(2) < most || t.device() != dev ||
       (t.size(2) > 1 && t.stride(2) != 1))
@@ -105,6 +113,7 @@ void rows_call(RowsCall call, const char* name, const Tensor& pool, const Tensor
 void kv_store(const Tensor& pool, const Tensor& k, const Tensor& v, const Tensor& table, const Tensor& cu, const OptTensor& start,
               const OptTensor& error) {
   if (k.dim() != 3) refuse("kv_store: k must have three dimensions");
+  no_gradient({&k, &v}, "kv_store");
   rows_call(moe_kv_store, "moe_kv_store", pool, k, v, table, cu, start, k.size(0), error);
 }
 
@@ -142,6 +151,7 @@ Tensor kv_attend(const Tensor& pool, const Tensor& q, const Tensor& table, const
   const moe_kv_table t = table_of(table, dev, "kv_attend: table");
   const int32_t* lens_p = ints(lens, 1, dev, "kv_attend: lens", t.n_seqs);
   if (q.dim() != 3) refuse("kv_attend: q must have three dimensions");
+  no_gradient({&q}, "kv_attend");
   const int64_t heads = q.size(1);
   const int64_t most = max_len ? *max_len : (int64_t)t.width * c.page_tokens;
   const auto type = q.scalar_type();
@@ -188,6 +198,7 @@ std::tuple<Tensor, Tensor, Tensor> kv_evict(const Tensor& pool, const Tensor& ta
 Tensor attend_prompt(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu, std::optional<double> scale,
                      const OptTensor& out_arg, const OptTensor& error) {
   if (!q.is_cuda() || q.dim() != 3 || k.dim() != 3) refuse("attend_prompt: q, k and v must be CUDA tensors of three dimensions");
+  no_gradient({&q, &k, &v}, "attend_prompt");
   const auto dev = q.device();
   const auto type = q.scalar_type();
   const int64_t n = q.size(0), heads = q.size(1), dim = q.size(2), kv = k.size(1);

@@ -166,3 +166,26 @@ def test_sequences_that_share_one_table_row(moe):
     assert new.tolist() == [16] * t and kept[0, 0, -4:].tolist() == [n - t - 3 + i for i in range(4)]
     with pytest.raises(moe.MoEError):  # but not to the same ones
         moe.kv_evict(more, shared, lens, n, score, 16, 4, tables(1, 1, first=c.pool.shape[0]).expand(t, -1))
+
+
+# ------------------------------------------------------------------ gradients
+
+
+@pytest.mark.parametrize("which", ["store", "attend", "prompt", "prompt values"])
+def test_rows_that_want_a_gradient_are_refused(moe, which):
+    """No gradient flows through these calls: a call that would lose one is refused, unless gradients are off."""
+    c = Cache(moe, [40], 2, 64, 16, FP)
+    q, k = rnd(1, 4, 64, dtype=FP).requires_grad_(), rnd(1, 2, 64, dtype=FP)
+    call = {
+        "store": lambda: moe.kv_store(c.pool, k, q[:, :2], c.table, ints([0, 1])),
+        "attend": lambda: moe.kv_attend(c.pool, q, c.table, c.lens),
+        "prompt": lambda: moe.attend_prompt(q, k, k, ints([0, 1])),
+        "prompt values": lambda: moe.attend_prompt(q.detach(), k, q[:, :2], ints([0, 1])),
+    }[which]
+    with pytest.raises(moe.MoEError) as e:
+        call()
+    assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+    with torch.no_grad():
+        call()
+    with torch.inference_mode():
+        call()
