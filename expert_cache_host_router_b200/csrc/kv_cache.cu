@@ -546,7 +546,8 @@ constexpr int kMoveTiles = 4;  // destination tiles of one CTA
 
 // Copies the kept rows to the destination pages: a row's bytes keep their place within a
 // tile row, so 16-byte pieces move whole (keys) or as the halves of two source pairs
-// (values).  Only bytes of rows below the new length are written.
+// (values).  Only bytes of rows below the new length are written.  A row whose page is not
+// there gets scales of NaN, so that nobody reads what was in its place before.
 template <int D>
 __global__ void __launch_bounds__(192) kv_move_kernel(const KvView c, const KvView o, const EvictArgs a) {
   constexpr int NB = D / 32, ROWS = kMoveTiles * kTileTok;
@@ -608,20 +609,20 @@ __global__ void __launch_bounds__(192) kv_move_kernel(const KvView c, const KvVi
       *to = r;
     } else if (p < 2 * PC + 16) {
       const int row = p - 2 * PC, i = t * kTileTok + row;
-      if (src[i]) {
+      if (i < n) {
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k)
           reinterpret_cast<uint32_t*>(d + 16 * D)[row * (NB / 2) + k] =
-              reinterpret_cast<const uint32_t*>(src[i] + 16 * D)[srow[i] * (NB / 2) + k];
+              src[i] ? reinterpret_cast<const uint32_t*>(src[i] + 16 * D)[srow[i] * (NB / 2) + k] : 0x7E007E00u;
       }
     } else {
       const int q = p - 2 * PC - 16, pair = q / NB, nb = q % NB;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = t * kTileTok + 2 * pair + e;
-        if (src[i])
+        if (i < n)
           reinterpret_cast<uint16_t*>(d + 17 * D)[q * 2 + e] =
-              reinterpret_cast<const uint16_t*>(src[i] + 17 * D)[((srow[i] >> 1) * NB + nb) * 2 + (srow[i] & 1)];
+              src[i] ? reinterpret_cast<const uint16_t*>(src[i] + 17 * D)[((srow[i] >> 1) * NB + nb) * 2 + (srow[i] & 1)] : 0x7E00;
       }
     }
   }

@@ -368,8 +368,9 @@ MOE_API int moe_decode_step_noalloc(const moe_config *cfg, const moe_noalloc_wei
  * them: the kernels do.  A row whose page number, position or length lies outside the
  * described cache is neither read nor written there; error_dev (when not NULL) receives
  * MOE_DEVERR_PAGE if it was 0, and the call's results for that row (moe_kv_load) or that
- * sequence and KV head (moe_kv_attend: its outputs and the scores added to) are NaN; a
- * length that cannot be counts as 0 in moe_kv_evict and leaves scores alone.  A device-side
+ * sequence and KV head (moe_kv_attend: its outputs and the scores added to) are NaN; in
+ * moe_kv_evict a kept row of such a page becomes NaN in its new place, and a length that
+ * cannot be counts as 0 and leaves scores alone.  A device-side
  * wait that runs out (2 s) sets MOE_DEVERR_TMA and gives NaN too.
  *
  * Limits (else MOE_ERR_UNSUPPORTED): 8192 sequences a call, 1024 KV heads, 1024 query

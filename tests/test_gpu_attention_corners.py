@@ -189,3 +189,34 @@ def test_rows_that_want_a_gradient_are_refused(moe, which):
         call()
     with torch.inference_mode():
         call()
+
+
+# ------------------------------------------------------------------ evict
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_evicted_rows_of_a_missing_page_are_nan(moe, dim):
+    """Kept rows whose page is not there do not leave what was in their new place before."""
+    n, keep = 80, 37
+    c = Cache(moe, [n, n], 2, dim, 16, BF, more=6)
+    score = torch.rand(2, 2, n, device=DEV)
+    out_table = tables(2, 3, first=c.table.numel())
+    moe.kv_store(c.pool, *(rnd(2 * 48, 2, dim, dtype=BF, seed=s) for s in (7, 8)), out_table, ints([0, 48, 96]))  # what was there before
+    before = moe.kv_load(c.pool, out_table, ints([0, 48, 96]), None, 96, F32)
+    table = c.table.clone()
+    table[0, 2] = -1                # positions 32..47 of the first sequence
+    err = ints([0])
+    new, kept, _ = moe.kv_evict(c.pool, table, c.lens, n, score, keep, 5, out_table, error=err)
+    assert int(err) == moe.MOE_DEVERR_PAGE and new.tolist() == [keep, keep]
+    after = moe.kv_load(c.pool, out_table, ints([0, 48, 96]), None, 96, F32)
+    for rows, got, was in ((c.k, *[x[0] for x in (after, before)]), (c.v, *[x[1] for x in (after, before)])):
+        for b in range(2):
+            for h in range(2):
+                for r in range(48):
+                    x = got[48 * b + r, h].double()
+                    if r >= keep:
+                        assert torch.equal(x, was[48 * b + r, h].double())
+                    elif b == 0 and 32 <= int(kept[b, h, r]) < 48:
+                        assert bool(x.isnan().all())
+                    else:
+                        assert torch.equal(x, rows[b][int(kept[b, h, r]), h])
