@@ -798,7 +798,7 @@ EncodeTiled encode_tiled() {
   static EncodeTiled fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+    if (!kv_ok(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q)) ||
         q != cudaDriverEntryPointSuccess)
       p = nullptr;
     return reinterpret_cast<EncodeTiled>(p);
@@ -909,5 +909,5 @@ extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_ro
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == MOE_BF16 ? prompt_pick<__nv_bfloat16>(a, mq, mk, mv, head_dim, device, st)
                                           : prompt_pick<__half>(a, mq, mk, mv, head_dim, device, st);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return kv_status(e);
 }

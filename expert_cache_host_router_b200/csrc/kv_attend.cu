@@ -990,21 +990,6 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   return MOE_OK;
 }
 
-static cudaError_t launch(void (*kernel)(const KvView, const AttendArgs), int grid, int threads, size_t smem,
-                          cudaStream_t st, bool dependent, const KvView& c, const AttendArgs& a) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, c, a);
-}
-
 template <typename T, int D, int NT>
 static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendPlan& p, int device, cudaStream_t st) {
   const int smem = AttendSmem<D, NT>::bytes(c.n_seqs);
@@ -1016,8 +1001,8 @@ static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendP
     if (e != cudaSuccess) return e;
     ready[device] = true;
   }
-  cudaError_t e = a.score ? launch(kv_attend_kernel<T, D, NT, true>, p.n_cta, kAW * 32, smem, st, false, c, a)
-                          : launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a);
+  cudaError_t e = a.score ? kv_launch(kv_attend_kernel<T, D, NT, true>, p.n_cta, kAW * 32, smem, st, false, c, a)
+                          : kv_launch(kv_attend_kernel<T, D, NT, false>, p.n_cta, kAW * 32, smem, st, false, c, a);
   if (e != cudaSuccess) return e;
   // Few items have many pieces each: a CTA for every head joins them; of many items each has a
   // piece or two, and a CTA joins all heads.  Us by head / by item, heads of 128: 4 items
@@ -1025,8 +1010,8 @@ static cudaError_t attend_go(const KvView& c, const AttendArgs& a, const AttendP
   // 80 / 51; scored calls 38 / 40, 21.3 / 18.4, 24.7 / 20.4, 41 / 32, 98 / 65.
   const bool heads = p.items < 32;  // (scores or not: the same bits)
   const int grid = (int)p.items * (heads ? 8 * NT : 1) + (a.score ? c.n_seqs * c.heads * p.score_ctas : 0);
-  return heads ? launch(kv_attend_join<T, D, NT, true>, grid, kJoinThreads, 0, st, true, c, a)
-               : launch(kv_attend_join<T, D, NT, false>, grid, kJoinThreads, 0, st, true, c, a);
+  return heads ? kv_launch(kv_attend_join<T, D, NT, true>, grid, kJoinThreads, 0, st, true, c, a)
+               : kv_launch(kv_attend_join<T, D, NT, false>, grid, kJoinThreads, 0, st, true, c, a);
 }
 
 }  // namespace moe
@@ -1098,5 +1083,5 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   if (c.dim == 64) e = p.nt == 1 ? MOE_GO(64, 1) : MOE_GO(64, 2);
   else e = p.nt == 1 ? MOE_GO(128, 1) : MOE_GO(128, 2);
 #undef MOE_GO
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return kv_status(e);
 }

@@ -631,15 +631,10 @@ __global__ void __launch_bounds__(192) kv_move_kernel(const KvView c, const KvVi
 // ------------------------------------------------------------------ entry points
 
 template <typename T, bool VEC>
-static void rows_launch(bool store, const KvView& c, const RowArgs& a, int n_tok, cudaStream_t st) {
-  const int grid = (a.n_tokens + n_tok - 1) / n_tok;
-  if (c.dim == 64) {
-    if (store) kv_store_kernel<T, 64, VEC><<<grid, 256, 0, st>>>(c, a, n_tok);
-    else kv_load_kernel<T, 64, VEC><<<grid, 256, 0, st>>>(c, a, n_tok);
-  } else {
-    if (store) kv_store_kernel<T, 128, VEC><<<grid, 256, 0, st>>>(c, a, n_tok);
-    else kv_load_kernel<T, 128, VEC><<<grid, 256, 0, st>>>(c, a, n_tok);
-  }
+static cudaError_t rows_launch(bool store, const KvView& c, const RowArgs& a, int n_tok, cudaStream_t st) {
+  const dim3 grid((a.n_tokens + n_tok - 1) / n_tok);
+  if (c.dim == 64) return kv_launch(store ? kv_store_kernel<T, 64, VEC> : kv_load_kernel<T, 64, VEC>, grid, 256, 0, st, false, c, a, n_tok);
+  return kv_launch(store ? kv_store_kernel<T, 128, VEC> : kv_load_kernel<T, 128, VEC>, grid, 256, 0, st, false, c, a, n_tok);
 }
 
 static int rows_call(bool store, const moe_kv_pool* cache, const moe_kv_table* table, const int32_t* cu,
@@ -670,15 +665,9 @@ static int rows_call(bool store, const moe_kv_pool* cache, const moe_kv_table* t
   int n_tok = 2;
   for (const int sms = kv_sm_count(cache->device); n_tok < kMaxTok && n_tokens > 4 * sms * n_tok;) n_tok *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == MOE_F32) {
-    if (vec) rows_launch<float, true>(store, c, a, n_tok, st); else rows_launch<float, false>(store, c, a, n_tok, st);
-  } else if (dtype == MOE_F16) {
-    if (vec) rows_launch<__half, true>(store, c, a, n_tok, st); else rows_launch<__half, false>(store, c, a, n_tok, st);
-  } else {
-    if (vec) rows_launch<__nv_bfloat16, true>(store, c, a, n_tok, st);
-    else rows_launch<__nv_bfloat16, false>(store, c, a, n_tok, st);
-  }
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (dtype == MOE_F32) return kv_status(vec ? rows_launch<float, true>(store, c, a, n_tok, st) : rows_launch<float, false>(store, c, a, n_tok, st));
+  if (dtype == MOE_F16) return kv_status(vec ? rows_launch<__half, true>(store, c, a, n_tok, st) : rows_launch<__half, false>(store, c, a, n_tok, st));
+  return kv_status(vec ? rows_launch<__nv_bfloat16, true>(store, c, a, n_tok, st) : rows_launch<__nv_bfloat16, false>(store, c, a, n_tok, st));
 }
 
 }  // namespace moe
@@ -719,18 +708,8 @@ extern "C" int moe_kv_evict(const moe_kv_pool* cache, const moe_kv_table* table,
   DeviceScope dev(cache->device);
   if (!dev.ok) return MOE_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  kv_select_kernel<<<c.n_seqs * c.heads, kSelThreads, 0, st>>>(c, a);
+  cudaError_t e = kv_launch(kv_select_kernel, dim3(c.n_seqs * c.heads), kSelThreads, 0, st, false, c, a);
   const dim3 grid((keep + kMoveTiles * kTileTok - 1) / (kMoveTiles * kTileTok), c.n_seqs * c.heads);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(192);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, c.dim == 64 ? kv_move_kernel<64> : kv_move_kernel<128>, c, o, a) == cudaSuccess ? MOE_OK
-                                                                                                               : MOE_ERR_CUDA;
+  if (e == cudaSuccess) e = kv_launch(c.dim == 64 ? kv_move_kernel<64> : kv_move_kernel<128>, grid, 192, 0, st, true, c, o, a);
+  return kv_status(e);
 }

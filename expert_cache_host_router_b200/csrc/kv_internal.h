@@ -34,13 +34,37 @@ struct KvView {  // a cache pool and its page table, as the kernels take them
   int32_t* error;  // or null
 };
 
+// Whether a runtime call went well.  One that did not is not left behind as the thread's last
+// error, where the next call's launches would find it.
+inline bool kv_ok(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess;
+}
+inline int kv_status(cudaError_t e) { return kv_ok(e) ? MOE_OK : MOE_ERR_CUDA; }
+
+// Launches a kernel and says how that launch went (the last error may be another call's).
+// dependent: the kernel may start up while the one before it in the stream runs.
+template <typename... P, typename... A>
+inline cudaError_t kv_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool dependent, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Current device for the length of a call.
 struct DeviceScope {
   int was = -1;
   bool ok = false;
   explicit DeviceScope(int dev) {
-    if (cudaGetDevice(&was) != cudaSuccess) return;
-    ok = was == dev || cudaSetDevice(dev) == cudaSuccess;
+    ok = kv_ok(cudaGetDevice(&was)) && (was == dev || kv_ok(cudaSetDevice(dev)));
     now = dev;
   }
   ~DeviceScope() {
@@ -65,7 +89,7 @@ inline int kv_sm_count(int dev) {
   static std::atomic<int> known[kKvMaxDevices];
   int n = known[dev].load(std::memory_order_relaxed);
   if (!n) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (!kv_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
     known[dev].store(n, std::memory_order_relaxed);
   }
   return n;

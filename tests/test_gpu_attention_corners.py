@@ -220,3 +220,40 @@ def test_evicted_rows_of_a_missing_page_are_nan(moe, dim):
                         assert bool(x.isnan().all())
                     else:
                         assert torch.equal(x, rows[b][int(kept[b, h, r]), h])
+
+
+# ------------------------------------------------------------------ errors
+
+
+def test_a_refused_call_leaves_nothing_behind(moe):
+    """A device that is not there: that call fails, the next good ones do not."""
+    import ctypes
+    P = ctypes.c_void_p
+    c = Cache(moe, [40], 2, 64, 16, FP, more=4)
+    k, cu, score = rnd(3, 2, 64, dtype=FP), ints([0, 3]), torch.zeros(1, 2, 48, device=DEV)
+    out_table = tables(1, 1, first=c.table.numel())
+    absent = moe.KvPool(c.pool.data_ptr(), c.pool.shape[0], 2, 64, 16, torch.cuda.device_count(), None)
+    table = moe.KvTable(c.table.data_ptr(), 1, c.table.shape[1], c.table.shape[1])
+    rows = moe.Rows(k.data_ptr(), k.stride(0), k.stride(1))
+
+    def fail():
+        L = moe.lib()
+        s = L.moe_kv_store(absent, table, P(cu.data_ptr()), None, rows, rows, 3, moe.MOE_F16, None)
+        a = L.moe_kv_attend_workspace(absent, table, 4, 40, 0, ctypes.c_size_t())
+        p = L.moe_attend_prompt(torch.cuda.device_count(), rows, rows, rows, moe.Rows(score.data_ptr(), 128, 64), P(cu.data_ptr()), 1, 3,
+                                2, 2, 64, moe.MOE_F16, 1.0, None, None)
+        assert (s, a, p) == (moe.MOE_ERR_CUDA,) * 3
+        with pytest.raises(moe.MoEError):
+            moe.moe_create(moe.Config(1, 256, 16, 2, 256, 0, 0, 0, 1e-6, torch.cuda.device_count(), 0, 0))
+
+    fail()
+    moe.kv_store(c.pool, k, k, c.table, cu)
+    fail()
+    moe.kv_load(c.pool, c.table, cu, None, 3, FP)
+    fail()
+    moe.kv_evict(c.pool, c.table, c.lens, 48, score, 16, 4, out_table)
+    fail()
+    moe.kv_attend(c.pool, rnd(1, 4, 64, dtype=FP), c.table, c.lens)
+    fail()
+    moe.attend_prompt(k, k, k, cu)
+    torch.cuda.synchronize()
