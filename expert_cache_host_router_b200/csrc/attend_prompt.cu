@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       // A part of the weights by a polynomial on the FMA pipe instead of the exponential unit was
       // tried (an eighth to a half of them): 1216..1255 against 1255 TFLOP/s, the issue slots being taken as well.
-      const float off = -m * a.scale2;
+      const float off = m == -INFINITY ? 0.0f : -m * a.scale2;  // products of -inf only, so far: no weight
       const uint64_t sc = f2(a.scale2, a.scale2), of = f2(off, off);
       uint64_t sum[4] = {0, 0, 0, 0};
       auto weights = [&](int c, uint32_t(&p)[16]) {

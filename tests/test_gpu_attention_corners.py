@@ -257,3 +257,21 @@ def test_a_refused_call_leaves_nothing_behind(moe):
     fail()
     moe.attend_prompt(k, k, k, cu)
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ prompts: what is not finite
+
+
+def test_prompt_keys_that_no_row_can_see(moe):
+    """A whole tile of keys with products of minus infinity has no weight; NaN in later keys reaches no earlier row."""
+    n, dim = 520, 64
+    q, k, v = rnd(n, 2, dim, dtype=BF, seed=1).abs(), rnd(n, 2, dim, dtype=BF, seed=2), rnd(n, 2, dim, dtype=BF, seed=3)
+    k[:200, 0, 3] = -float("inf")
+    k[400, 1] = float("nan")
+    q[:, :, 3] = 1.0
+    out = moe.attend_prompt(q, k, v, ints([0, n]))
+    assert bool(out[:200, 0].isnan().all()) and bool(out[400:, 1].isnan().all())
+    # without the rows of no weight
+    shifted = out[200:, :1]
+    check_rows(shifted, q[200:, :1], k[200:, :1], v[200:, :1], 0, n - 200, list(range(n - 200)), dim ** -0.5)
+    check_rows(out[:, 1:], q[:, 1:], k[:, 1:], v[:, 1:], 0, 400, list(range(400)), dim ** -0.5)
