@@ -44,6 +44,8 @@ struct PromptArgs {
   int64_t o_tok, o_head;
   int vec;
   int32_t* error;
+  const void *q, *k, *v;  // the rows themselves: see mend_rows
+  int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
 };
 
 __device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
@@ -206,6 +208,20 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return r;
 }
 
+// acc + 0 * p of two 16-bit values: no longer 0 once one of them is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t odd2(uint32_t p, uint32_t acc);
+template <>
+__device__ __forceinline__ uint32_t odd2<__half>(uint32_t p, uint32_t acc) {
+  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(p), "r"(0u));
+  return acc;
+}
+template <>
+__device__ __forceinline__ uint32_t odd2<__nv_bfloat16>(uint32_t p, uint32_t acc) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(p), "r"(0u));
+  return acc;
+}
+
 // Pairs of fp32: one instruction for two.
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
   uint64_t r;
@@ -256,6 +272,73 @@ __device__ __forceinline__ int prompt_blocks(const PromptArgs& a, int b, int* ro
   *row = s;
   *rows = n;
   return (n + 2 * kPM - 1) / (2 * kPM);
+}
+
+// Rows of one query tile whose output is not finite because of a value behind them.  On the
+// diagonal the weights of later keys are 0, but 0 times an infinity or NaN is NaN in the product: it
+// would reach up to 127 rows before that value's.  The warp finds where each channel's first
+// value that is not finite stands in the diagonal tile and computes the channels of rows before it
+// again, key by key from memory.  (Rows from it on are not finite by definition.)  Nothing of
+// this runs while values are finite; a row of 16384 keys takes a warp about a millisecond.
+template <typename T, int D, int COLS>
+__device__ __forceinline__ void mend_rows(const PromptArgs& a, const PromptItem& it, int tile0, int r, bool odd, float m, float inv, int ch0) {
+  constexpr int C = COLS / 32;  // channels of a lane, one after the other
+  struct __align__(2 * C) Some { T x[C]; };
+  const int lane = threadIdx.x & 31, kh = it.head / a.group;
+  const T* v = static_cast<const T*>(a.v) + it.row0 * a.v_tok + kh * a.v_head + ch0 + C * lane;
+  const T* k = static_cast<const T*>(a.k) + it.row0 * a.k_tok + kh * a.k_head;
+  const int end = min(tile0 + kPN, it.n);
+  int first[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) first[i] = end;
+#pragma unroll 8
+  for (int j = end - 1; j >= tile0; --j) {
+    const Some y = *reinterpret_cast<const Some*>(v + j * a.v_tok);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (!isfinite(to_float(y.x[i]))) first[i] = j;
+  }
+  uint32_t rows = __ballot_sync(0xffffffffu, odd && r < it.n && isfinite(inv));
+#pragma unroll 1
+  for (; rows; rows &= rows - 1) {
+    const int src = __ffs(rows) - 1, row = __shfl_sync(0xffffffffu, r, src);
+    bool need[C], any = false;
+#pragma unroll
+    for (int i = 0; i < C; ++i) any |= need[i] = first[i] > row && first[i] < end;
+    if (!__any_sync(0xffffffffu, any)) continue;
+    const float mr = __shfl_sync(0xffffffffu, m, src), fr = __shfl_sync(0xffffffffu, inv, src);
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (it.row0 + row) * a.q_tok + it.head * a.q_head);
+    float o[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = 0.0f;
+#pragma unroll 1
+    for (int j0 = row; j0 >= 0; j0 -= 32) {  // 32 keys at a time, the nearest first: a lane's product, then all lanes' values
+      const uint4* kj = reinterpret_cast<const uint4*>(k + max(j0 - lane, 0) * a.k_tok);
+      float s = 0.0f;
+#pragma unroll 8
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = q[c], y = kj[c];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(to_float(reinterpret_cast<const T*>(&x)[i]), to_float(reinterpret_cast<const T*>(&y)[i]), s);
+      }
+      const float w = lane <= j0 ? ex2((s - mr) * a.scale2) : 0.0f;  // (behind key 0: its value again, with no weight)
+#pragma unroll 16
+      for (int e = 0; e < 32; ++e) {
+        const float we = __shfl_sync(0xffffffffu, w, e);
+        const Some y = *reinterpret_cast<const Some*>(v + max(j0 - e, 0) * a.v_tok);
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = fmaf(we, to_float(y.x[i]), o[i]);
+      }
+      bool done = true;
+#pragma unroll
+      for (int i = 0; i < C; ++i) done &= !need[i] || o[i] != o[i];
+      if (__all_sync(0xffffffffu, done)) break;  // a NaN before this tile
+    }
+    T* dst = static_cast<T*>(a.out) + (int64_t)(it.row0 + row) * a.o_tok + it.head * a.o_head + ch0 + C * lane;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (need[i]) dst[i] = from_float<T>(o[i] * fr);
+  }
 }
 
 template <int D>
@@ -522,12 +605,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
          f0 = m == top ? 1.0f : ex2((m - top) * a.scale2);
          f1 = m1 == top ? 1.0f : ex2((m1 - top) * a.scale2);
          l = l * f0 + l1 * f1;
+         m = top;
        }
        ++merges;
      }
      const float inv = ok ? 1.0f / l : __int_as_float(0x7fc00000);
      if (!ok && lane == 0) kv_flag(a.error, MOE_DEVERR_TMA);
      T* dst = static_cast<T*>(a.out) + (int64_t)(it.row0 + r) * a.o_tok + it.head * a.o_head + rank * COLS;
+     uint32_t odd = 0;
 #pragma unroll 1
      for (int c = 0; c < COLS; c += 32) {
        uint32_t o[32];
@@ -552,6 +637,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
          uint32_t p[16];
 #pragma unroll
          for (int i = 0; i < 16; ++i) p[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+         for (int i = 0; i < 16; ++i) odd = odd2<T>(p[i], odd);
          if (a.vec) {
 #pragma unroll
            for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
@@ -560,6 +647,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
            for (int i = 0; i < 32; ++i) reinterpret_cast<uint16_t*>(dst + c)[i] = (uint16_t)(p[i >> 1] >> (16 * (i & 1)));
          }
        }
+     }
+     if (__any_sync(0xffffffffu, odd != 0)) {
+       __syncwarp();  // the rows are written: what follows writes some of their channels again
+       mend_rows<T, D, COLS>(a, it, it.block * 2 * kPM + w * kPM, r, odd != 0, m, inv, rank * COLS);
      }
      if (CL > 1) {  // Q's place may be loaded again
        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -906,6 +997,9 @@ extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_ro
   a.o_head = out->head_stride;
   a.vec = kv_align_ok(out->data_dev, 16) && out->token_stride % 8 == 0 && out->head_stride % 8 == 0;
   a.error = error_dev;
+  a.q = q->data_dev, a.q_tok = q->token_stride, a.q_head = q->head_stride;
+  a.k = k->data_dev, a.k_tok = k->token_stride, a.k_head = k->head_stride;
+  a.v = v->data_dev, a.v_tok = v->token_stride, a.v_head = v->head_stride;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == MOE_BF16 ? prompt_pick<__nv_bfloat16>(a, mq, mk, mv, head_dim, device, st)
                                           : prompt_pick<__half>(a, mq, mk, mv, head_dim, device, st);

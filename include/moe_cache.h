@@ -484,9 +484,10 @@ MOE_API int moe_kv_evict(const moe_kv_pool *cache, const moe_kv_table *table, co
  * MOE_BF16 or MOE_F16; q, k and v 16-byte aligned with strides that are multiples of 8
  * elements above 0 (else MOE_ERR_UNSUPPORTED; the stride of a single row or head is not looked at).  out may not overlap q, k or v.  scale > 0.  Rows
  * outside every sequence are left as they were.
- * Products and sums are fp32, the weights are rounded to dtype.  A value row that is not
- * finite makes rows of its own sequence from its tile of 128 positions on NaN, also those
- * before it in that tile; never rows of another sequence.  A sequence whose bounds are not
+ * Products and sums are fp32, the weights are rounded to dtype.  A value that is not finite
+ * makes its channel not finite from its own row on; it reaches no row before it and none of
+ * another sequence (up to 127 rows before it are computed again, key by key, which takes longer).
+ * A sequence whose bounds are not
  * 0 <= cu[b] <= cu[b + 1] <= n_tokens is skipped and sets error_dev (may be NULL). */
 MOE_API int moe_attend_prompt(int32_t device, const moe_rows *q, const moe_rows *k, const moe_rows *v,
                               const moe_rows *out, const int32_t *cu_dev, int32_t n_seqs, int32_t n_tokens,

@@ -275,3 +275,31 @@ def test_prompt_keys_that_no_row_can_see(moe):
     shifted = out[200:, :1]
     check_rows(shifted, q[200:, :1], k[200:, :1], v[200:, :1], 0, n - 200, list(range(n - 200)), dim ** -0.5)
     check_rows(out[:, 1:], q[:, 1:], k[:, 1:], v[:, 1:], 0, 400, list(range(400)), dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim,hq,hkv,lens", [(64, 4, 2, [300]), (128, 2, 1, [129, 1, 700]), (128, 2, 1, [2500]), (64, 3, 3, [100, 5000])])
+def test_prompt_values_that_are_not_finite_reach_no_earlier_row(moe, dtype, dim, hq, hkv, lens):
+    n = sum(lens)
+    q = rnd(n, hq, dim, dtype=dtype, seed=1, std=2.0)
+    k, v = rnd(n, hkv, dim, dtype=dtype, seed=2), rnd(n, hkv, dim, dtype=dtype, seed=3)
+    first, m = starts(lens)[-2], lens[-1]
+    bad = m - 70                      # with rows of its tile of 128 on both sides
+    v2 = v.clone()
+    v2[first + bad, 0] = float("nan")
+    if hkv > 1:
+        v2[first + bad, 1, 5] = float("inf")
+    v2[first + bad + 20, 0, 7] = -float("inf")
+    out = moe.attend_prompt(q, k, v2, ints(starts(lens)))
+    g = hq // hkv
+    for a, x in zip(starts(lens), lens):
+        if a != first:
+            check_rows(out, q, k, v, a, x, list(range(x)), dim ** -0.5)
+    check_rows(out, q, k, v, first, m, sorted({*range(max(0, bad - 140), bad), *range(0, bad, 37)}), dim ** -0.5)
+    assert bool(out[first + bad:first + m, :g].isnan().all())
+    if hkv > 1:
+        row = out[first + bad:first + m, g:2 * g]
+        assert not bool(row[..., 5].isfinite().any())
+        rest = [c for c in range(dim) if c != 5]
+        clean = moe.attend_prompt(q, k, v, ints(starts(lens)))[first + bad:first + m, g:2 * g]
+        assert bool(row[..., rest].isfinite().all()) and bool((row[..., rest].float() - clean[..., rest].float()).abs().max() < 2 ** -6)
