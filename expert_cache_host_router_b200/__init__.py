@@ -144,6 +144,7 @@ _SIGS = {
                                     _P, _P, _P, _P]),
     "moe_attend_prompt": (ctypes.c_int, [ctypes.c_int32] + [ctypes.POINTER(Rows)] * 4 + [_P] + [ctypes.c_int32] * 6
                           + [ctypes.c_float, _P, _P]),
+    "moe_debug_stall_attention": (ctypes.c_int, [ctypes.c_int32]),
     "moe_destroy": (None, [_P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }

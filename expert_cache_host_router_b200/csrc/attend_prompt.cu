@@ -43,6 +43,7 @@ struct PromptArgs {
   void* out;
   int64_t o_tok, o_head;
   int vec;
+  int stall;  // for tests: the first CTA (or pair) is never given its item of this number (0: it is given all)
   int32_t* error;
   const void *q, *k, *v;  // the rows themselves: see mend_rows
   int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
@@ -341,6 +342,44 @@ __device__ __forceinline__ void mend_rows(const PromptArgs& a, const PromptItem&
   }
 }
 
+// Items of this CTA (or pair), in order, by a whole warp; f says whether to go on.  s, n and mine:
+// prompt_blocks of the sequence of this lane's number.
+//
+// Longest first: blocks by their number within the sequence (the key tiles they need), the
+// last ones first; of those with the same number all sequences that have it, of each all
+// heads side by side (they share keys and values).  Of every gridDim items in that order a
+// CTA takes one, from the front and from the back in turn (from the front alone, the first
+// CTA has the longest each time: 880 us against 814 for one prompt of 16384 tokens).
+template <int CL, typename F>
+__device__ __forceinline__ void each_item(const PromptArgs& a, int s, int n, int mine, F&& f) {
+  const int lane = threadIdx.x & 31;
+  int most = __reduce_max_sync(0xffffffffu, mine);
+  for (int b = 32; b < a.n_seqs; b += 32) {
+    mine = prompt_blocks(a, b + lane, &s, &n);
+    most = max(most, __reduce_max_sync(0xffffffffu, mine));
+  }
+  int64_t before = 0, want = blockIdx.x / CL;  // items before the sequences looked at; the next one wanted
+  const int64_t step = gridDim.x / CL;
+  bool ok = true;
+  const bool few = a.n_seqs <= 32;  // then every lane keeps its sequence
+  for (int q = most - 1; q >= 0 && ok; --q) {
+    for (int b = 0; b < a.n_seqs && ok; b += 32) {
+      if (!few) mine = prompt_blocks(a, b + lane, &s, &n);
+      const uint32_t has = __ballot_sync(0xffffffffu, mine > q);
+      const int64_t here = (int64_t)__popc(has) * a.n_heads;
+      while (want < before + here && ok) {
+        const int k = (int)(want - before) / a.n_heads, head = (int)(want - before) % a.n_heads;
+        // the k-th sequence that has this block
+        const int src = __ffs(__ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == k)) - 1;
+        ok = f(PromptItem{__shfl_sync(0xffffffffu, s, src), __shfl_sync(0xffffffffu, n, src), q, head});
+        const int64_t round = want / step;
+        want = (round + 2) * step - 1 - (want - round * step);
+      }
+      before += here;
+    }
+  }
+}
+
 template <int D>
 struct PromptSmem {
   static constexpr int kStages = D == 64 ? 4 : 2;
@@ -383,7 +422,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint64_t *item_full = v_empty + ST, *item_empty = item_full + 2;
   // pairs: S of an item done here; Q's place free at the other CTA; its halves arrived; ours read
   uint64_t *s_all = item_empty + 2, *peer_ready = s_all + 1, *merge_full = s_all + 2, *merged = s_all + 4;
-  PromptItem* items = reinterpret_cast<PromptItem*>(s_all + 5);
+  uint64_t* drained = s_all + 5;  // after a wait that ran out: the products of each MMA warp are through
+  PromptItem* items = reinterpret_cast<PromptItem*>(s_all + 7);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_at + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -409,6 +449,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     bar_init(merge_full, 4);
     bar_init(merge_full + 1, 4);
     bar_init(merged, 8);
+    bar_init(drained, 1);
+    bar_init(drained + 1, 1);
     for (int i = 0; i < ST; ++i) {
       bar_init(k_full + i, 1);
       bar_init(k_empty + i, 1);
@@ -661,7 +703,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else if (warp == 8) {
     // ---------------------------------------------------------------- TMA
     bool ok = true;
-    int kv = 0, fixes = 0, loads[2] = {0, 0};  // key tiles, cleared tails and query tiles so far
+    int kv = 0, ks = 0, fixes = 0, loads[2] = {0, 0};  // tiles of values, of keys, cleared tails and query tiles so far
     int products = 0;                          // items with key tiles of this CTA's so far
     for (int turn = 0; ok; ++turn) {
       const PromptItem it = take(turn);
@@ -687,6 +729,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           bar_expect(k_full + s, S::kTileB);
           for (int c = 0; c < NB; ++c) tma3(ka + s * S::kTileB + c * S::kBox, &mk, 64 * c, kh, key0, k_full + s);
         }
+        ++ks;
         if (round) ok = bar_wait(v_empty + s, (round - 1) & 1, abort);
         if (!ok) break;
         const int left = it.n - (j * CL + rank) * kPN;  // keys of this tile that are the sequence's
@@ -718,6 +761,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (ok && n_kv) ok = bar_wait(s_all, products++ & 1, abort);
         if (ok && lane == 0) peer_arrive(peer_addr(peer_ready, rank ^ 1));
       }
+    }
+    if (__any_sync(0xffffffffu, *abort)) {  // what was asked for may still be on its way (each wait ends soon now)
+      for (int w = 0; w < 2; ++w) bar_wait(q_full + w, (loads[w] - 1) & 1, abort);
+      for (int s = 0; s < ST; ++s) {  // the last round of each stage; -1, a phase that is over, if there was none
+        bar_wait(k_full + s, (ks > s ? (ks - 1 - s) / ST : -1) & 1, abort);
+        bar_wait(v_full + s, (ks > s ? (ks - 1 - s) / ST : -1) & 1, abort);
+      }
+      bar_wait(fix, fixes & 1, abort);
     }
   } else if (warp < 11) {
     // ---------------------------------------------------------------- MMA
@@ -831,52 +882,44 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
     }
+    if (__any_sync(0xffffffffu, *abort)) {
+      if (leader) commit(drained + warp - 9);
+      __syncwarp();
+      bar_wait(drained + warp - 9, 0, abort);
+    }
   } else {
     // ---------------------------------------------------------------- items
-    // Longest first: blocks by their number within the sequence (the key tiles they need), the
-    // last ones first; of those with the same number all sequences that have it, of each all
-    // heads side by side (they share keys and values).  Of every gridDim items in that order a
-    // CTA takes one, from the front and from the back in turn (from the front alone, the first
-    // CTA has the longest each time: 880 us against 814 for one prompt of 16384 tokens).
-    int s = seq_row, n = seq_rows, mine = seq_blocks, most = __reduce_max_sync(0xffffffffu, mine);
-    for (int b = 32; b < a.n_seqs; b += 32) {
-      mine = prompt_blocks(a, b + lane, &s, &n);
-      most = max(most, __reduce_max_sync(0xffffffffu, mine));
-    }
     int turn = 0;
-    int64_t before = 0, want = blockIdx.x / CL;  // items before the sequences looked at; the next one wanted
-    const int64_t step = gridDim.x / CL;
     bool ok = true;
     auto give = [&](const PromptItem& it) {
       if (turn > 1) ok = bar_wait(item_empty + (turn & 1), ((turn >> 1) - 1) & 1, abort);
+      if (a.stall && turn == a.stall && blockIdx.x < CL) ok = false;
       if (ok && lane == 0) {
         items[turn & 1] = it;
         bar_arrive(item_full + (turn & 1));
       }
       ++turn;
+      return ok;
     };
-    const bool few = a.n_seqs <= 32;  // then every lane keeps its sequence
-    for (int q = most - 1; q >= 0 && ok; --q) {
-      for (int b = 0; b < a.n_seqs && ok; b += 32) {
-        if (!few) mine = prompt_blocks(a, b + lane, &s, &n);
-        const uint32_t has = __ballot_sync(0xffffffffu, mine > q);
-        const int64_t here = (int64_t)__popc(has) * a.n_heads;
-        while (want < before + here && ok) {
-          const int k = (int)(want - before) / a.n_heads, head = (int)(want - before) % a.n_heads;
-          // the k-th sequence that has this block
-          const int src = __ffs(__ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == k)) - 1;
-          give(PromptItem{__shfl_sync(0xffffffffu, s, src), __shfl_sync(0xffffffffu, n, src), q, head});
-          const int64_t round = want / step;
-          want = (round + 2) * step - 1 - (want - round * step);
-        }
-        before += here;
-      }
-    }
+    each_item<CL>(a, seq_row, seq_rows, seq_blocks, give);
     if (ok) give(PromptItem{-1, 0, 0, 0});
   }
   tc_before();
   __syncwarp();
   __syncthreads();
+  if (warp == 11 && *abort) {
+    // A wait ran out: what this CTA has to write is not valid, or not there at all.
+    kv_flag(a.error, MOE_DEVERR_TMA);
+    int s, n;
+    const int mine = prompt_blocks(a, lane, &s, &n);
+    each_item<CL>(a, s, n, mine, [&](const PromptItem& it) {
+      constexpr int COLS = D / CL;
+      const int first = it.block * 2 * kPM, rows = min(2 * kPM, it.n - first);
+      T* dst = static_cast<T*>(a.out) + (int64_t)(it.row0 + first) * a.o_tok + it.head * a.o_head + rank * COLS;
+      for (int i = lane; i < rows * COLS; i += 32) dst[i / COLS * a.o_tok + i % COLS] = from_float<T>(__int_as_float(0x7fc00000));
+      return true;
+    });
+  }
   if (CL > 1) cluster_sync();  // neither leaves while the other may still write to it
   if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
@@ -957,6 +1000,19 @@ cudaError_t prompt_pick(const PromptArgs& a, const CUtensorMap& mq, const CUtens
 
 using namespace moe;
 
+static std::atomic<int> g_stalls{0};  // calls that are still to run into their waits' limits
+int moe::kv_stall() {
+  int n = g_stalls.load(std::memory_order_relaxed);
+  while (n > 0 && !g_stalls.compare_exchange_weak(n, n - 1)) {
+  }
+  return n > 0;
+}
+extern "C" int moe_debug_stall_attention(int32_t n) {
+  if (n < 0) return MOE_ERR_INVALID;
+  g_stalls = n;
+  return MOE_OK;
+}
+
 extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_rows* k, const moe_rows* v, const moe_rows* out,
                                  const int32_t* cu_dev, int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads,
                                  int32_t n_kv_heads, int32_t head_dim, int32_t dtype, float scale, int32_t* error_dev,
@@ -997,6 +1053,7 @@ extern "C" int moe_attend_prompt(int32_t device, const moe_rows* q, const moe_ro
   a.o_head = out->head_stride;
   a.vec = kv_align_ok(out->data_dev, 16) && out->token_stride % 8 == 0 && out->head_stride % 8 == 0;
   a.error = error_dev;
+  a.stall = kv_stall();
   a.q = q->data_dev, a.q_tok = q->token_stride, a.q_head = q->head_stride;
   a.k = k->data_dev, a.k_tok = k->token_stride, a.k_head = k->head_stride;
   a.v = v->data_dev, a.v_tok = v->token_stride, a.v_head = v->head_stride;

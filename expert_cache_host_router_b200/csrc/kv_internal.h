@@ -73,6 +73,8 @@ struct DeviceScope {
   int now = -1;
 };
 
+int kv_stall();  // 1 if this call is to run into its waits' limits (moe_debug_stall_attention)
+
 constexpr int kKvMaxDevices = 64;
 constexpr int kKvMaxSeqs = 8192;
 constexpr int kKvMaxPos = INT32_MAX - 4095;  // positions, lengths and rows: roundings up to whole tiles stay in 32 bits

@@ -371,7 +371,8 @@ MOE_API int moe_decode_step_noalloc(const moe_config *cfg, const moe_noalloc_wei
  * sequence and KV head (moe_kv_attend: its outputs and the scores added to) are NaN; in
  * moe_kv_evict a kept row of such a page becomes NaN in its new place, and a length that
  * cannot be counts as 0 and leaves scores alone.  A device-side
- * wait that runs out (2 s) sets MOE_DEVERR_TMA and gives NaN too.
+ * wait that runs out (about 2 s) sets MOE_DEVERR_TMA and gives NaN too (moe_attend_prompt: in all
+ * rows that the CTA in question computes).
  *
  * Limits (else MOE_ERR_UNSUPPORTED): 8192 sequences a call, 1024 KV heads, 1024 query
  * heads a KV head, 65535 sequences x KV heads in moe_kv_evict, 2^31 - 4096 positions a sequence,
@@ -493,6 +494,11 @@ MOE_API int moe_attend_prompt(int32_t device, const moe_rows *q, const moe_rows 
                               const moe_rows *out, const int32_t *cu_dev, int32_t n_seqs, int32_t n_tokens,
                               int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t dtype, float scale,
                               int32_t *error_dev, void *stream);
+
+/* Fault injection for tests: the next n calls of moe_attend_prompt (of the whole process) never
+ * give their first CTA, or pair of CTAs, its second piece of work, so that its bounded waits run
+ * out (no GPU fault involved; such a call takes seconds). */
+MOE_API int moe_debug_stall_attention(int32_t n);
 
 /* Free everything.  NULL is a no-op. */
 MOE_API void moe_destroy(moe_ctx *ctx);

@@ -12,3 +12,7 @@ def test_one_table_row_for_all_sequences(lib):
         assert lib.moe_kv_store(c, table(row_stride=bad), P, None, rows(), rows(), 0, 0, None) == INVALID
     s = moe.KvScore(P, 512, 256)
     assert lib.moe_kv_evict(c, t, P, 100, s, 16, 4, table(table_dev=2 * P, row_stride=0), 3 * P, P, P, None) == INVALID
+
+
+def test_stalls_asked_for(lib):
+    assert lib.moe_debug_stall_attention(-1) == INVALID and lib.moe_debug_stall_attention(0) == moe.MOE_OK

@@ -9,6 +9,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from test_gpu_attention import BF, DEV, F32, FP, Cache, check_attend, half, ints, moe, quantised, rnd, starts, tables  # noqa: E402,F401
+from prompt_items import turns  # noqa: E402
 from test_prompt_items import SHORT_AMONG_LONG, SMS  # noqa: E402
 
 
@@ -303,3 +304,30 @@ def test_prompt_values_that_are_not_finite_reach_no_earlier_row(moe, dtype, dim,
         rest = [c for c in range(dim) if c != 5]
         clean = moe.attend_prompt(q, k, v, ints(starts(lens)))[first + bad:first + m, g:2 * g]
         assert bool(row[..., rest].isfinite().all()) and bool((row[..., rest].float() - clean[..., rest].float()).abs().max() < 2 ** -6)
+
+
+# ------------------------------------------------------------------ waits that run out
+
+
+@pytest.mark.parametrize("dim,heads,lens", [(64, 100, [700]), (128, 4, [100, 8092])])
+def test_prompt_wait_that_runs_out(moe, dim, heads, lens):
+    """A CTA (or pair) that never gets its next item: all its rows are NaN, the error word says so, other
+    rows are what they are without, and the next call is good."""
+    n = sum(lens)
+    q, k, v = rnd(n, heads, dim, dtype=BF, seed=1), rnd(n, heads, dim, dtype=BF, seed=2), rnd(n, heads, dim, dtype=BF, seed=3)
+    cu, err = ints(starts(lens)), ints([0])
+    want = moe.attend_prompt(q, k, v, cu, error=err)
+    assert int(err) == 0
+    out = torch.full_like(q, 3.0)
+    assert moe.lib().moe_debug_stall_attention(1) == moe.MOE_OK
+    moe.attend_prompt(q, k, v, cu, out=out, error=err)
+    torch.cuda.synchronize()
+    assert int(err) == 3  # MOE_DEVERR_TMA
+    nan = torch.zeros(n, heads, dtype=torch.bool, device=DEV)
+    for s, block, h in turns(lens, heads, SMS)[1][0]:
+        a = starts(lens)[s]
+        nan[a + 256 * block:min(a + 256 * (block + 1), a + lens[s]), h] = True
+    assert nan.any() and not nan.all()
+    assert bool(out[nan].isnan().all()) and torch.equal(out[~nan], want[~nan])
+    err.zero_()
+    assert torch.equal(moe.attend_prompt(q, k, v, cu, error=err), want) and int(err) == 0
