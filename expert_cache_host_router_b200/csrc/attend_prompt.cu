@@ -70,16 +70,25 @@ __device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// By whole warps.  False after 2^21 attempts of at most about a microsecond each, or soon after
-// another role gave up.  Inline: a call here would make the softmax warps save their row of
-// products.  Most phases are over when they are asked for: a test and a vote then take some 55
+__device__ __forceinline__ uint32_t now_ns() {  // wraps after 4.3 s
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// By whole warps.  False after 2 s, or soon after another role gave up.  (An attempt that fails takes
+// about 4 us, so a count of attempts is a poor clock.)  Inline: a call here would make the softmax
+// warps save their row of products.  Most phases are over when they are asked for: a test and a vote then take some 55
 // cycles, an attempt with a time and a loop that each lane leaves by itself 170 (16384 tokens:
 // 817 -> 802 us; 4 heads of 64, 8192 tokens: 72 -> 69).
+constexpr uint32_t kLimitNs = 2000000000u;
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
   if (__all_sync(0xffffffffu, bar_test(b, parity))) return true;
-  for (int i = 0; i < (1 << 21); ++i) {
+  const uint32_t t0 = now_ns();
+  for (uint32_t i = 1;; ++i) {
     if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
-    if ((i & 1023) == 1023 && __any_sync(0xffffffffu, *abort)) return false;
+    if (i % 256) continue;
+    if (__any_sync(0xffffffffu, *abort)) return false;
+    if (__any_sync(0xffffffffu, now_ns() - t0 > kLimitNs)) break;
   }
   *abort = 1;
   return false;
@@ -173,9 +182,12 @@ __device__ __forceinline__ bool peer_try(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ bool peer_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-  for (int i = 0; i < (1 << 21); ++i) {
+  const uint32_t t0 = now_ns();
+  for (uint32_t i = 1;; ++i) {
     if (__all_sync(0xffffffffu, peer_try(b, parity))) return true;
-    if ((i & 1023) == 1023 && __any_sync(0xffffffffu, *abort)) return false;
+    if (i % 256) continue;
+    if (__any_sync(0xffffffffu, *abort)) return false;
+    if (__any_sync(0xffffffffu, now_ns() - t0 > kLimitNs)) break;
   }
   *abort = 1;
   return false;

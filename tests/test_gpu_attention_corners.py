@@ -2,6 +2,7 @@
 
 Against 64 bits, with the tolerances that tests/test_gpu_attention.py derives."""
 import math
+import time
 
 import pytest
 
@@ -320,8 +321,10 @@ def test_prompt_wait_that_runs_out(moe, dim, heads, lens):
     assert int(err) == 0
     out = torch.full_like(q, 3.0)
     assert moe.lib().moe_debug_stall_attention(1) == moe.MOE_OK
+    t = time.monotonic()
     moe.attend_prompt(q, k, v, cu, out=out, error=err)
     torch.cuda.synchronize()
+    assert 1.5 < time.monotonic() - t < 4  # the limit is 2 s
     assert int(err) == 3  # MOE_DEVERR_TMA
     nan = torch.zeros(n, heads, dtype=torch.bool, device=DEV)
     for s, block, h in turns(lens, heads, SMS)[1][0]:
