@@ -44,6 +44,7 @@ struct AttendArgs {
   int min_run;                   // tiles a CTA takes at least
   int score_ctas;                // CTAs of a sequence's and KV head's scores
   int vec;                       // rows of q can be read 8 bytes at a time
+  uint32_t stall;                // for tests: bytes that every copy is expected to have more than it has
   float* part;                   // [2 CTAs][8 NT][D] partial outputs, unnormalised
   float* ml;                     // [2 CTAs][8 NT][2] their (m, l)
   float* ml_whole;               // [items][8 NT][2] (m, l) of the items that one CTA has whole (scored calls)
@@ -109,18 +110,19 @@ __device__ __forceinline__ bool kv_mbar_try(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// False when the copy has not landed within 2 s.
-__device__ __noinline__ bool kv_mbar_spin(uint64_t* bar, uint32_t parity) {
+// False when the copy has not landed within so many ns.
+constexpr uint64_t kLimitNs = 2000000000ull;
+__device__ __noinline__ bool kv_mbar_spin(uint64_t* bar, uint32_t parity, uint64_t limit) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   while (!kv_mbar_try(bar, parity)) {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    if (t - t0 > 2000000000ull) return false;
+    if (t - t0 > limit) return false;
   }
   return true;
 }
 
-// One bulk copy into shared memory.  Cache rows are read once per step: evict first.
+// One bulk copy into shared memory.
 __device__ __forceinline__ void kv_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(kv_smem(bar))
@@ -301,13 +303,13 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
       uint8_t* dst = ring + stage * S::kStage;
       const uint8_t* src = c.pool + (int64_t)tile_a * S::kTile;
       if (tile_a >= 0 && tile_b == tile_a + 1) {
-        kv_expect(bars + stage, 2 * S::kTile);
+        kv_expect(bars + stage, 2 * S::kTile + a.stall);
         kv_bulk(kv_smem(dst), src, 2 * S::kTile, bars + stage);
       } else {
         // a missing page's keys get NaN scales, which makes the row's output NaN
         if (tile_a < 0 || tile_b == -1)
           for (int i = 0; i < D / 2; ++i) reinterpret_cast<uint16_t*>(dst + 16 * D + (tile_a < 0 ? 0 : S::kTile))[i] = 0x7E00;
-        kv_expect(bars + stage, (tile_a >= 0 ? S::kTile : 0) + (tile_b >= 0 ? S::kTile : 0));
+        kv_expect(bars + stage, (tile_a >= 0 ? S::kTile : 0) + (tile_b >= 0 ? S::kTile : 0) + a.stall);
         if (tile_a >= 0) kv_bulk(kv_smem(dst), src, S::kTile, bars + stage);
         if (tile_b >= 0) kv_bulk(kv_smem(dst + S::kTile), c.pool + (int64_t)tile_b * S::kTile, S::kTile, bars + stage);
       }
@@ -424,9 +426,11 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
     int left = min(attend_len(c, a, sg.b), sg.s1 * kTileTok) - key0;
     float* zrow = SCORED ? a.z + ((int64_t)(sg.b * items + sg.item) * a.max_len + key0) * COLS + 2 * t : nullptr;
     for (; n_groups > 0; --n_groups, left -= kGT * kTileTok) {
-      if (alive && !kv_mbar_try(bars + stage, phase) && !kv_mbar_spin(bars + stage, phase)) {
-        alive = false;
+      if (alive && !kv_mbar_try(bars + stage, phase) && !kv_mbar_spin(bars + stage, phase, kLimitNs)) {
+        alive = false;  // all that this warp has left becomes NaN; it asks for nothing more
         kv_flag(c.error, MOE_DEVERR_TMA);
+        // and lets what it asked for arrive, for up to 10 ms each, before its shared memory may be another CTA's
+        for (int s = 0; s < ST; ++s) kv_mbar_spin(bars + s, s >= stage ? phase : phase ^ 1, 10000000ull);
       }
       const uint8_t* base = ring + stage * S::kStage;
       const bool tail = left < kGT * kTileTok;
@@ -593,7 +597,8 @@ __global__ void __launch_bounds__(kAW * 32, NT == 1 ? 2 : 1) kv_attend_kernel(co
       // Every lane has read the stage; the fence orders those reads before the copy engine's write.
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      issue(stage);
+      alive = __all_sync(0xffffffffu, alive);
+      if (alive) issue(stage);
       if (SCORED) zrow += kGT * kTileTok * COLS;
       if (++stage == ST) {
         stage = 0;
@@ -1062,6 +1067,7 @@ extern "C" int moe_kv_attend(const moe_kv_pool* cache, const moe_kv_table* table
   a.scale2 = scale * 1.4426950408889634f;
   a.min_run = p.min_run;
   a.score_ctas = p.score_ctas;
+  a.stall = kv_stall();
   a.vec = kv_align_ok(q->data_dev, 8) && q->token_stride % 4 == 0 && q->head_stride % 4 == 0;
   a.part = reinterpret_cast<float*>(ws + p.part);
   a.ml = reinterpret_cast<float*>(ws + p.ml);

@@ -495,9 +495,10 @@ MOE_API int moe_attend_prompt(int32_t device, const moe_rows *q, const moe_rows 
                               int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t dtype, float scale,
                               int32_t *error_dev, void *stream);
 
-/* Fault injection for tests: the next n calls of moe_attend_prompt (of the whole process) never
- * give their first CTA, or pair of CTAs, its second piece of work, so that its bounded waits run
- * out (no GPU fault involved; such a call takes seconds). */
+/* Fault injection for tests: in the next n calls of moe_attend_prompt and moe_kv_attend (of the
+ * whole process) bounded waits run out, with no GPU fault involved: the first CTA, or pair of CTAs, of
+ * moe_attend_prompt is never given its second piece of work, and every copy of moe_kv_attend is
+ * expected to be longer than it is.  Such a call takes 2 s and more. */
 MOE_API int moe_debug_stall_attention(int32_t n);
 
 /* Free everything.  NULL is a no-op. */

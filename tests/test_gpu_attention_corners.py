@@ -334,3 +334,24 @@ def test_prompt_wait_that_runs_out(moe, dim, heads, lens):
     assert bool(out[nan].isnan().all()) and torch.equal(out[~nan], want[~nan])
     err.zero_()
     assert torch.equal(moe.attend_prompt(q, k, v, cu, error=err), want) and int(err) == 0
+
+
+@pytest.mark.parametrize("dim,group,scored", [(64, 2, True), (128, 16, False)])
+def test_attend_wait_that_runs_out(moe, dim, group, scored):
+    """Copies that never come as long as they should be: NaN, the error word, and the next call is good."""
+    lens = [300, 0, 17, 2000]
+    c = Cache(moe, lens, 2, dim, 16, BF)
+    q = rnd(4, 2 * group, dim, dtype=BF, seed=5)
+    err, score = ints([0]), torch.zeros(4, 2, 2000, device=DEV)
+    want = moe.kv_attend(c.pool, q, c.table, c.lens, 2000, error=err)
+    assert moe.lib().moe_debug_stall_attention(1) == moe.MOE_OK
+    t = time.monotonic()
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, 2000, score=score if scored else None, error=err)
+    torch.cuda.synchronize()
+    assert 1.5 < time.monotonic() - t < 4
+    assert int(err) == 3  # MOE_DEVERR_TMA
+    for b, n in enumerate(lens):
+        assert bool(out[b].isnan().all()) if n else torch.equal(out[b], torch.zeros_like(out[b]))
+        assert bool((score[b, :, n:] == 0).all()) and (not scored or bool(score[b, :, :n].isnan().all()))
+    err.zero_()
+    assert torch.equal(moe.kv_attend(c.pool, q, c.table, c.lens, 2000, error=err), want) and int(err) == 0
