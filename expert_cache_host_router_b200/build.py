@@ -33,13 +33,24 @@ def _stale() -> bool:
 
 
 def _build_bind(force: bool) -> None:
-    deps = [BIND_SRC, os.path.join(ROOT, "include", "moe_cache.h")]
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(d) for d in deps):
-        return
+    """The extension module, where torch and its headers are there (the library needs neither).  Rebuilt
+    when its sources, torch or the interpreter are other ones."""
     import sysconfig
-
-    import torch
-    from torch.utils.cpp_extension import include_paths, library_paths
+    try:
+        import torch
+        from torch.utils.cpp_extension import include_paths, library_paths
+    except ImportError:
+        return
+    if not any(os.path.exists(os.path.join(i, "torch", "extension.h")) for i in include_paths()):
+        return
+    deps = [BIND_SRC, os.path.join(ROOT, "include", "moe_cache.h")]
+    made_with = f"{torch.__version__} {sysconfig.get_config_var('SOABI')}\n"
+    stamp = BIND + ".stamp"
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(d) for d in deps):
+        if os.path.exists(stamp):
+            with open(stamp) as f:
+                if f.read() == made_with:
+                    return
     inc = include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
                              os.path.join(ROOT, "include")]
     tmp = BIND + f".{os.getpid()}.tmp"
@@ -48,6 +59,9 @@ def _build_bind(force: bool) -> None:
                            *[f"-I{i}" for i in inc], BIND_SRC, "-o", tmp, *[f"-L{p}" for p in library_paths()], f"-L{OUT_DIR}",
                            "-l:libmoe.so", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BIND)
+    with open(stamp + f".{os.getpid()}.tmp", "w") as f:
+        f.write(made_with)
+    os.replace(f.name, stamp)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
