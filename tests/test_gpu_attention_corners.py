@@ -355,3 +355,52 @@ def test_attend_wait_that_runs_out(moe, dim, group, scored):
         assert bool((score[b, :, n:] == 0).all()) and (not scored or bool(score[b, :, :n].isnan().all()))
     err.zero_()
     assert torch.equal(moe.kv_attend(c.pool, q, c.table, c.lens, 2000, error=err), want) and int(err) == 0
+
+
+# ------------------------------------------------------------------ several host threads
+
+
+def test_calls_from_several_threads(moe):
+    """Four host threads, each with a stream and buffers of its own, at the same time; the C calls are made
+    without the interpreter's lock."""
+    import ctypes
+    import threading
+    P, L = ctypes.c_void_p, moe.lib()
+    sets = []
+    for s in range(4):
+        c = Cache(moe, [300 + 100 * s, 17], 2, 64, 16, FP, seed=s)
+        q = rnd(2, 8, 64, dtype=FP, seed=5 + s)
+        p = [rnd(400, h, 64, dtype=FP, seed=s + h) for h in (4, 2, 2)]
+        want = moe.kv_attend(c.pool, q, c.table, c.lens), moe.attend_prompt(*p, ints([0, 400]))
+        sets.append((c, q, p, ints([0, 400]), want))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, q, p, cu, want):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(50):
+                a = moe.kv_attend(c.pool, q, c.table, c.lens, stream=stream)
+                b = moe.attend_prompt(*p, cu, stream=stream)
+                with torch.cuda.stream(stream):
+                    d = torch.zeros_like(p[0])
+                r = [moe.Rows(x.data_ptr(), x.stride(0), x.stride(1)) for x in (*p, d)]
+                if L.moe_attend_prompt(0, *r, P(cu.data_ptr()), 1, 400, 4, 2, 64, moe.MOE_F16, 0.125, None, P(stream.cuda_stream)):
+                    bad.append("status")
+                try:
+                    moe.kv_attend(c.pool, q.float(), c.table, c.lens)
+                    bad.append("not refused")
+                except moe.MoEError:
+                    pass
+                stream.synchronize()
+                if not (torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(d, want[1])):
+                    bad.append("differs")
+        except Exception as e:  # noqa: BLE001
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=s) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not bad, bad
