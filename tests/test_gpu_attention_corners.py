@@ -404,3 +404,108 @@ def test_calls_from_several_threads(moe):
     for t in threads:
         t.join(60)
     assert not bad, bad
+
+
+# ------------------------------------------------------------------ the ends of the documented ranges
+
+
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("most", [0, 1, 33])
+def test_attend_batch_without_positions(moe, scored, most):
+    c = Cache(moe, [0, 0, 0], 2, 64, 16, BF, more=1)
+    q, score = rnd(3, 8, 64, dtype=BF, seed=5), torch.ones(3, 2, 40, device=DEV)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, most, score=score if scored else None)
+    assert not bool(out.any()) and bool((score == 1).all())
+
+
+@pytest.mark.parametrize("dim,heads,group,scored", [(128, 1, 8, False), (128, 1, 12, True), (64, 2, 1, True)])
+def test_attend_most_sequences(moe, dim, heads, group, scored):
+    """8192 sequences, most of them empty or of one position: the longest table of starts in shared memory."""
+    lens = [0 if i % 3 else i % 40 for i in range(8192)]
+    c = Cache(moe, lens, heads, dim, 16, FP)
+    q, score = rnd(8192, heads * group, dim, dtype=FP, seed=5), torch.zeros(8192, heads, 39, device=DEV)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, 39, score=score if scored else None)
+    for b in (0, 1, 3, 39, 2000, 4095, 4098, 8189, 8190, 8191):
+        check_attend(out, score.double() if scored else None, q, c, b, dim ** -0.5)
+    assert bool(out.isfinite().all())
+
+
+def test_attend_most_query_heads(moe):
+    c = Cache(moe, [100, 3], 1, 64, 16, BF)
+    q, score = rnd(2, 1024, 64, dtype=BF, seed=5), torch.zeros(2, 1, 100, device=DEV)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, 100, score=score)
+    for b in range(2):
+        check_attend(out, None, q, c, b, 0.125)
+    assert abs(float(score.double().sum()) - 2048) < 2048 * 2.0 ** -12
+
+
+@pytest.mark.parametrize("seqs", [1, 254, 255, 256, 257, 8192])
+def test_store_and_load_of_many_sequences(moe, seqs):
+    lens = [(i * 7) % 4 for i in range(seqs)]
+    lens[-1] = 3
+    start = [(i * 5) % 30 for i in range(seqs)]
+    n = sum(lens)
+    k, v = rnd(n, 1, 64, dtype=BF, seed=1), rnd(n, 1, 64, dtype=BF, seed=2)
+    table = tables(seqs, 3)
+    pool = moe.kv_pool(table.numel(), 16, 1, 64)
+    err = ints([0])
+    moe.kv_store(pool, k, v, table, ints(starts(lens)), ints(start), error=err)
+    gk, gv = moe.kv_load(pool, table, ints(starts(lens)), ints(start), n, F32, error=err)
+    assert int(err) == 0 and torch.equal(gk.double(), quantised(k)) and torch.equal(gv.double(), quantised(v))
+
+
+def test_large_pages_and_many_kv_heads(moe):
+    lens = [5000, 1, 4096]
+    c = Cache(moe, lens, 40, 64, 4096, FP)
+    q = rnd(3, 80, 64, dtype=FP, seed=5)
+    out = moe.kv_attend(c.pool, q, c.table, c.lens, 5000)
+    for b in range(3):
+        check_attend(out, None, q, c, b, 0.125)
+
+
+@pytest.mark.parametrize("seqs", [31, 32, 33, 8192])
+def test_prompt_many_sequences(moe, seqs):
+    lens = [(i * 3) % 5 for i in range(seqs)]
+    lens[seqs // 2] = 700
+    n = sum(lens)
+    q, k, v = rnd(n, 4, 64, dtype=FP, seed=1), rnd(n, 1, 64, dtype=FP, seed=2), rnd(n, 1, 64, dtype=FP, seed=3)
+    out = moe.attend_prompt(q, k, v, ints(starts(lens)))
+    cu = starts(lens)
+    for s in sorted({0, 1, seqs // 2 - 1, seqs // 2, seqs // 2 + 1, seqs - 2, seqs - 1}):
+        if lens[s]:
+            check_rows(out, q, k, v, cu[s], lens[s], list(range(lens[s])), 0.125)
+    assert bool(out.isfinite().all())
+
+
+def test_graphs_of_two_streams_at_once(moe):
+    """Two captured steps, each with buffers of its own, replayed on two streams without waiting in between."""
+    def step(seed):
+        c = Cache(moe, [700 + seed, 33], 2, 64, 16, FP, seed=seed, more=8)
+        q, score = rnd(2, 8, 64, dtype=FP, seed=5 + seed), torch.zeros(2, 2, 720, device=DEV)
+        p = [rnd(300, h, 64, dtype=FP, seed=seed + h) for h in (4, 2, 2)]
+        cu, out_table = ints([0, 300]), tables(2, 4, first=c.table.numel())
+        # everything the step allocates is made in here
+        def run():
+            score.zero_()
+            o = moe.kv_attend(c.pool, q, c.table, c.lens, 720, score=score)
+            n, kept, s = moe.kv_evict(c.pool, c.table, c.lens, 720, score, 50, 9, out_table)
+            k, v = moe.kv_load(c.pool, out_table, ints_cu, None, 83, FP)
+            return o, n, kept, s, k, v, moe.attend_prompt(*p, cu)
+        ints_cu = ints([0, 50, 83])
+        return run
+    runs = [step(1), step(4)]
+    want = [[x.clone() for x in r()] for r in runs]
+    torch.cuda.synchronize()
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for r in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = r()
+        graphs.append((g, got))
+    for _ in range(30):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, got), w in zip(graphs, want):
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
