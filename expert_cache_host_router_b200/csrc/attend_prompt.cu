@@ -362,6 +362,9 @@ __device__ __forceinline__ void mend_rows(const PromptArgs& a, const PromptItem&
 // heads side by side (they share keys and values).  Of every gridDim items in that order a
 // CTA takes one, from the front and from the back in turn (from the front alone, the first
 // CTA has the longest each time: 880 us against 814 for one prompt of 16384 tokens).
+// Up to 32 sequences a lane keeps its own; of more, all bounds are read again for every block
+// number: one prompt of 16384 tokens among 31 or 33 short ones takes 790 us, among 1000 1360,
+// among 8000 7900 (8000 short ones alone 3300).
 template <int CL, typename F>
 __device__ __forceinline__ void each_item(const PromptArgs& a, int s, int n, int mine, F&& f) {
   const int lane = threadIdx.x & 31;

@@ -976,6 +976,8 @@ static int attend_plan(const KvView& c, int device, int n_q_heads, int max_len, 
   p->score_ctas = (int)(rows * per <= 16 * sms ? per : rows < 16 * sms ? 16 * sms / rows : 1);
   if (p->items * 8 * p->nt + (scored ? rows * p->score_ctas : 0) > kKvMaxPos) return MOE_ERR_UNSUPPORTED;
   const int64_t most = (tiles + p->min_run - 1) / p->min_run;
+  // (Two CTAs an SM fit as long as the starts of the sequences do: up to 471 with heads of 128. From there on
+  // they run one after the other: 471 sequences of 1000 positions, 4 groups of 8 heads, 96 us, 472 134.)
   int fill = (p->nt == 1 ? 2 : 1) * sms;
   if (fill > kJoinMax) fill = kJoinMax;
   p->n_cta = (int)(most < fill ? (most ? most : 1) : fill);

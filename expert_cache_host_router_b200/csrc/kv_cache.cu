@@ -155,12 +155,14 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int j, uint32_t 
     const float m = __uint_as_float((key & 0x7FFFE000u) | key << 31);
     const bool nan = (key & 0x7FFFE000u) > 0x7F800000u;
     d = nan ? __int_as_float(0x7fc00000) : fminf(fmaxf(m * -0.125f, -8188.0f), 8188.0f);
-    float inv = d == 0.0f ? 0.0f : __frcp_rn(d), y[8];
+    float inv = __frcp_rn(d), y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i];
-    if (!std::is_same<T, __half>::value && fabsf(inv) > 0x1p100f) {
+    if (std::is_same<T, __half>::value) {
+      if (d == 0.0f) inv = 0.0f;
+    } else if (key < 0x0F000000u) {  // below 2^-97
       // 1 / d may be beyond fp32 here: both sides 2^64 times as large, which changes no code
-      inv = __frcp_rn(d * 0x1p64f);
+      inv = d == 0.0f ? 0.0f : __frcp_rn(d * 0x1p64f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = x[i] * 0x1p64f;
     }

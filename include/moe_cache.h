@@ -428,7 +428,7 @@ typedef struct {
  * below cu_dev[0] and from cu_dev[n_seqs] on are padding and not read.  Only the bytes of
  * the rows' own positions change.  Rows of one call that fall on the same place of the same
  * page (a page named twice) leave that place unspecified.  For 16-bit rows the stored bytes are
- * the definition's exactly; for fp32 rows d and x / d are rounded to fp32 first.  dtype: MOE_BF16, MOE_F16 or
+ * the definition's exactly; for fp32 rows d, x / d and its sum with 8.5 are rounded to fp32.  dtype: MOE_BF16, MOE_F16 or
  * MOE_F32. */
 MOE_API int moe_kv_store(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *cu_dev,
                          const int32_t *start_dev, const moe_rows *k, const moe_rows *v, int32_t n_tokens,
@@ -451,7 +451,9 @@ MOE_API int moe_kv_load(const moe_kv_pool *cache, const moe_kv_table *table, con
  * KV head h, j < len; entries from len on are not touched.  Softmax statistics and sums
  * are fp32; the cached values are rounded to fp16 (q - 8) * d and the weights to fp16.
  * workspace: 16-byte aligned device memory of at least moe_kv_attend_workspace bytes,
- * contents irrelevant; calls that may overlap need one each.  The same call gives the same
+ * contents irrelevant; calls that may overlap need one each.  With score it holds every product
+ * that max_len allows, 4 bytes for each sequence, position and query head (a KV head's counted up to a multiple
+ * of 8, above 8 of 16): 1 GiB for 64 sequences of up to 131072 positions with 4 KV heads.  The same call gives the same
  * bits every time (no atomics); where a long sum is split depends on all lengths of the
  * call, so a sequence's last bits may differ between batches. */
 MOE_API int moe_kv_attend(const moe_kv_pool *cache, const moe_kv_table *table, const int32_t *len_dev,
