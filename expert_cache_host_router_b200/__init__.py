@@ -489,7 +489,8 @@ def kv_load(pool, table, cu, start, n_tokens: int, dtype, out=None, error=None, 
 def kv_attend(pool, q, table, lens, max_len=None, scale=None, score=None, out=None, workspace=None, error=None,
               stream=None):
     """Attention of one token per sequence, q [sequences, query heads, head dim] (bf16 or
-    fp16), over the first lens[b] cached positions of each.  max_len: an upper bound of lens
+    fp16), over the first lens[b] cached positions of each.  table may be one row expanded over the
+    sequences (several new tokens of one sequence).  max_len: an upper bound of lens
     known here (default: all that table holds); scale: default head_dim ** -0.5.  score:
     float32 [sequences, KV heads, >= max_len], to which every position's weight, summed
     over the query heads of its KV head, is added.  workspace: contiguous tensor of at least
@@ -526,7 +527,8 @@ def attend_prompt(q, k, v, cu, scale=None, out=None, error=None, stream=None):
     KV heads, head dim] (bf16 or fp16), sequence b being rows cu[b] .. cu[b + 1] - 1 (cu: int32
     [sequences + 1]).  scale: default head_dim ** -0.5.  Returns out (q's shape and type);
     rows outside every sequence are left as they were (unspecified in a tensor made here).
-    error: int32 [1], MOE_DEVERR_PAGE when a sequence's bounds are outside the rows."""
+    A value that is not finite reaches no row before its own.  error: int32 [1], MOE_DEVERR_PAGE
+    when a sequence's bounds are outside the rows."""
     f = (_bind_module or _bind()).attend_prompt
     if stream is None:
         return f(q, k, v, cu, scale, out, error)
